@@ -415,6 +415,131 @@ NVFP4_API nvfp4_status nvfp4_amax_accumulate(float* buf, const float* observed, 
 NVFP4_API nvfp4_status nvfp4_amax_accumulate_reduce(float* buf, const float* observed, int64_t n,
                                           float decay, void* stream);
 
+/* ------------------------------------------------------------------ MXFP4
+ *
+ * MXFP4 holds a vector in blocks of 32 elements: E2M1 codes packed two per
+ * byte (element 2i in the low nibble) and one E8M0 code c per block, standing
+ * for the scale 2^(c - 127); it needs no outer amax.  (OCP Microscaling
+ * Formats specification, v1.0.)  For a block with largest magnitude A,
+ *   c = clamp(floor(log2 A) - 2 + 127, 0, 254), c = 0 for A = 0;
+ *   code_i = E2M1(v_i / 2^(c - 127)), nearest, ties to even, at most 6.
+ * A block that holds an infinity or a NaN gets c = 255: it stands for 32 NaNs
+ * whatever its codes (which are then unspecified), and makes the outputs that
+ * use it NaN.  gfx950's matrix cores take this format directly.
+ *
+ * Layout of R vectors of K elements, with Kp = K rounded up to 128:
+ *   q   [R][Kp / 2] bytes; the codes past K are 0;
+ *   sf  [cdiv(R, 128)][Kp / 128][128][4] bytes: vector r's scale codes of
+ *       elements 128 t .. 128 t + 127 are the word sf[r / 128][t][r % 128].
+ *       Vectors past R in the last 128 have words of 0 where a cast without
+ *       groups writes them; no product reads them into an output.
+ * "Rowwise" vectors are the rows of x [M][K]; "columnwise" ones are its
+ * columns (K vectors of M elements, Mp = M rounded up to 128).  A product sums
+ * over the vectors' elements, so a linear layer y = x W^T with W [N][K] takes
+ * x and W rowwise, dx = dy W takes dy rowwise and W columnwise, and
+ * dW = dy^T x takes both columnwise.
+ *
+ * Shared rules: q and workspace 16-byte aligned, sf, offsets, rows and
+ * row_scale 4-byte, x and out to their type (EALIGN); counts of rows at most
+ * 2^31 - 1 and a sum's length K at most 2^23 (ESHAPE), as for launches of more
+ * than 2^31 - 1 tiles; negative sizes, unknown types and missing pointers are
+ * EINVAL; a call with nothing to write does nothing.  Any other size and any
+ * row pitch of x is accepted.  Every call writes all of its outputs (with
+ * groups: of every row that a group holds), deterministically, and may be
+ * captured into a graph.
+ */
+typedef enum {
+    NVFP4_F32 = 0,
+    NVFP4_BF16 = 1,
+    NVFP4_F16 = 2
+} nvfp4_dtype;
+
+/*
+ * MXFP4 cast of x [M][K] (row pitch ldx elements, columns adjacent), rowwise
+ * and / or columnwise from one read of x: pass NULL for both pointers of a
+ * direction that is not wanted.
+ */
+NVFP4_API nvfp4_status nvfp4_mx_quantize(const void* x, nvfp4_dtype type, int64_t M, int64_t K, int64_t ldx,
+                               uint8_t* row_q, uint8_t* row_sf, uint8_t* col_q, uint8_t* col_sf,
+                               void* stream);
+
+/*
+ * The same of R vectors in groups (the tokens of an expert each): vector r is
+ * row r of x, or with `rows` (int32 [R], device) row rows[r] of x, a row of
+ * zeros where that lies outside [0, M).  Group e holds the vectors
+ * offsets[e] <= r < offsets[e + 1] (int32 [num_groups + 1], device, read by
+ * the kernels: no host copy is needed; values are held to [0, R], and a group
+ * that ends before it begins is empty).  Rowwise outputs are those of
+ * nvfp4_mx_quantize on the R vectors.  Columnwise, each group starts a new
+ * 128-element step: with Tp = 128 * ((R + 127 min(num_groups, R)) / 128),
+ * col_q is [K][Tp / 2] and col_sf [cdiv(K, 128)][Tp / 128][128][4], group e
+ * filling the cdiv(count, 128) steps after those of the groups before it, its
+ * last step padded with codes and scales of 0.  Steps past the last group's
+ * are not written.
+ */
+NVFP4_API nvfp4_status nvfp4_mx_quantize_grouped(const void* x, nvfp4_dtype type, int64_t M, int64_t K, int64_t ldx,
+                                       const int32_t* rows, int64_t R, const int32_t* offsets,
+                                       int32_t num_groups, uint8_t* row_q, uint8_t* row_sf,
+                                       uint8_t* col_q, uint8_t* col_sf, void* stream);
+
+/* out [R][C] (fp32, bf16 or fp16, rounded to nearest-even) from R vectors of C elements. */
+NVFP4_API nvfp4_status nvfp4_mx_dequantize(const uint8_t* q, const uint8_t* sf, int64_t R, int64_t C,
+                                 nvfp4_dtype out_type, void* out, void* stream);
+
+/*
+ * out[m][n] = sum_k a[m][k] b[n][k] for M vectors a and N vectors b of K
+ * elements; out [M][N], summed in fp32 and rounded once to out_type.  K == 0
+ * gives zeros.
+ */
+NVFP4_API nvfp4_status nvfp4_mx_gemm(const uint8_t* a_q, const uint8_t* a_sf, const uint8_t* b_q, const uint8_t* b_sf,
+                           int64_t M, int64_t N, int64_t K, nvfp4_dtype out_type, void* out, void* stream);
+
+/*
+ * Grouped product: for the rows r of group e (offsets as above),
+ *   out[r][n] = row_scale[r] * sum_k a[rows[r]][k] b_e[n][k]
+ * with out [R][N], a of A vectors, and b holding num_groups operands of N
+ * vectors one after another (q [num_groups][N][Kp / 2], sf
+ * [num_groups][cdiv(N, 128)][Kp / 128][128][4]).  rows == NULL: R == A and
+ * row r is a[r]; an index outside [0, A) stands for a row of zeros.
+ * row_scale (fp32 [R]) == NULL: no factor.  Rows of out in no group are not
+ * written.
+ */
+NVFP4_API nvfp4_status nvfp4_mx_gemm_grouped(const uint8_t* a_q, const uint8_t* a_sf, int64_t A, const int32_t* rows,
+                                   int64_t R, const int32_t* offsets, int32_t num_groups,
+                                   const uint8_t* b_q, const uint8_t* b_sf, int64_t N, int64_t K,
+                                   const float* row_scale, nvfp4_dtype out_type, void* out, void* stream);
+
+/*
+ * The groups' weight gradients: out[e][n][k] = sum over the vectors r of group
+ * e of a[n][r] b[k][r], from the columnwise outputs of nvfp4_mx_quantize_grouped
+ * with the same R, offsets and num_groups (a of N vectors, b of K, both of the
+ * Tp elements stated there; Tp % 128 == 0, else ESHAPE).  out [num_groups][N][K];
+ * an empty group gives zeros.
+ */
+NVFP4_API nvfp4_status nvfp4_mx_wgrad_grouped(const uint8_t* a_q, const uint8_t* a_sf, const uint8_t* b_q,
+                                    const uint8_t* b_sf, int64_t N, int64_t K, int64_t Tp,
+                                    const int32_t* offsets, int32_t num_groups, nvfp4_dtype out_type,
+                                    void* out, void* stream);
+
+/*
+ * y = Q(x) W^T in one call: x [M][K] is cast rowwise on the way, W is N
+ * vectors; the result is that of nvfp4_mx_quantize and nvfp4_mx_gemm.
+ * workspace: device memory of nvfp4_mx_linear_workspace(M, N, K) bytes (may be
+ * 0; unspecified contents, free again once the call's work is done).
+ */
+NVFP4_API int64_t nvfp4_mx_linear_workspace(int64_t M, int64_t N, int64_t K);
+NVFP4_API nvfp4_status nvfp4_mx_linear(const void* x, nvfp4_dtype x_type, int64_t M, int64_t K, int64_t ldx,
+                             const uint8_t* w_q, const uint8_t* w_sf, int64_t N, nvfp4_dtype out_type,
+                             void* out, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* The same for nvfp4_mx_gemm_grouped, each row of x cast once however many groups it is in. */
+NVFP4_API int64_t nvfp4_mx_linear_grouped_workspace(int64_t M, int64_t R, int64_t N, int64_t K);
+NVFP4_API nvfp4_status nvfp4_mx_linear_grouped(const void* x, nvfp4_dtype x_type, int64_t M, int64_t K, int64_t ldx,
+                                     const int32_t* rows, int64_t R, const int32_t* offsets,
+                                     int32_t num_groups, const uint8_t* w_q, const uint8_t* w_sf,
+                                     int64_t N, const float* row_scale, nvfp4_dtype out_type, void* out,
+                                     void* workspace, int64_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -33,7 +33,10 @@ EXPORTS = ("nvfp4_abi_version", "nvfp4_last_error", "nvfp4_quantize", "nvfp4_qua
            "nvfp4_trace_encode", "nvfp4_quantize_calibrate", "nvfp4_quantize_sr", "nvfp4_gemm",
            "nvfp4_gemm_grouped", "nvfp4_quantize_rht", "nvfp4_swizzle_scales",
            "nvfp4_gemm_swizzled", "nvfp4_quantize_swizzled", "nvfp4_set_schedule",
-           "nvfp4_test_fail_next_wait")
+           "nvfp4_test_fail_next_wait", "nvfp4_mx_quantize", "nvfp4_mx_quantize_grouped",
+           "nvfp4_mx_dequantize", "nvfp4_mx_gemm", "nvfp4_mx_gemm_grouped", "nvfp4_mx_wgrad_grouped",
+           "nvfp4_mx_linear", "nvfp4_mx_linear_workspace", "nvfp4_mx_linear_grouped",
+           "nvfp4_mx_linear_grouped_workspace")
 
 STATUS = {0: "OK", 1: "EINVAL", 2: "ESHAPE", 3: "EALIGN", 4: "EDEVICE"}
 
@@ -78,6 +81,16 @@ def lib() -> ctypes.CDLL:
         "nvfp4_gemm_swizzled": (st, [p, p, p, ctypes.c_int, p, p, p, ctypes.c_int, i64, i64, i64, p, p]),
         "nvfp4_set_schedule": (st, [st]),
         "nvfp4_test_fail_next_wait": (st, []),
+        "nvfp4_mx_quantize": (st, [p, st, i64, i64, i64, p, p, p, p, p]),
+        "nvfp4_mx_quantize_grouped": (st, [p, st, i64, i64, i64, p, i64, p, i32, p, p, p, p, p]),
+        "nvfp4_mx_dequantize": (st, [p, p, i64, i64, st, p, p]),
+        "nvfp4_mx_gemm": (st, [p, p, p, p, i64, i64, i64, st, p, p]),
+        "nvfp4_mx_gemm_grouped": (st, [p, p, i64, p, i64, p, i32, p, p, i64, i64, p, st, p, p]),
+        "nvfp4_mx_wgrad_grouped": (st, [p, p, p, p, i64, i64, i64, p, i32, st, p, p]),
+        "nvfp4_mx_linear": (st, [p, st, i64, i64, i64, p, p, i64, st, p, p, i64, p]),
+        "nvfp4_mx_linear_workspace": (i64, [i64, i64, i64]),
+        "nvfp4_mx_linear_grouped": (st, [p, st, i64, i64, i64, p, i64, p, i32, p, p, i64, p, st, p, p, i64, p]),
+        "nvfp4_mx_linear_grouped_workspace": (i64, [i64, i64, i64, i64]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(L, name)
@@ -573,3 +586,7 @@ def set_schedule(schedule):
     if v not in (0, 1, 2):
         raise ValueError(f"unknown schedule {schedule!r}")
     _check(lib().nvfp4_set_schedule(v))
+
+
+from .mx import (mx_dequantize, mx_gemm, mx_gemm_grouped, mx_linear, mx_linear_grouped,  # noqa: E402
+                 mx_padded_rows, mx_quantize, mx_quantize_grouped, mx_sf_shape, mx_wgrad_grouped)

@@ -5,43 +5,17 @@
 
 #include <hip/hip_runtime.h>
 
-#include <cstdarg>
-#include <cstdio>
 #include <atomic>
 #include <mutex>
-#include <string>
 #include <vector>
 
 #include "nvfp4_device.hpp"
 #include "nvfp4_internal.h"
+#include "nvfp4_status.h"
 
 using namespace nvfp4;
 
 namespace {
-
-thread_local std::string g_last_error;
-
-nvfp4_status fail(nvfp4_status st, const char* fmt, ...) {
-    char buf[512];
-    va_list ap;
-    va_start(ap, fmt);
-    vsnprintf(buf, sizeof buf, fmt, ap);
-    va_end(ap);
-    g_last_error = buf;
-    return st;
-}
-
-nvfp4_status ok() {
-    g_last_error.clear();
-    return NVFP4_OK;
-}
-
-nvfp4_status check_hip(hipError_t e, const char* what) {
-    if (e != hipSuccess) return fail(NVFP4_EDEVICE, "%s: %s", what, hipGetErrorString(e));
-    return NVFP4_OK;
-}
-
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 struct Dir {
     bool want;

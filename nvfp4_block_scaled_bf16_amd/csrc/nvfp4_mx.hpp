@@ -1,0 +1,183 @@
+// nvfp4_mx.hpp -- MXFP4 on gfx950: what the cast (nvfp4_mx_cast.hip) and the
+// products (nvfp4_mx_gemm.hip) share.
+//
+// A vector is held in blocks of 32 elements along the dimension that a product
+// sums over: E2M1 codes, two per byte, and one E8M0 code c per block, standing
+// for the scale 2^(c - 127); c = 255 makes the whole block NaN.  For a block
+// with largest magnitude A,
+//   c = clamp(floor(log2 A) - 2 + 127, 0, 254),   0 for A = 0,
+//   code_i = E2M1(v_i / 2^(c - 127)), nearest, ties to even, at most 6.
+// (2 is the exponent of E2M1's largest binade, 4 .. 6.)  gfx950's scaled MFMA
+// multiplies such blocks directly, each lane giving 32 codes and their scale.
+//
+// Layout of R vectors of K elements, Kp = K rounded up to 128, Kt = Kp / 128:
+//   q  [R][Kp / 2] bytes, codes past K are 0;
+//   sf [cdiv(R, 128)][Kt][128][4]: the four scale codes of one vector's 128
+//      elements are one 32-bit word, and the words of 128 vectors are
+//      contiguous, so that a 128-row operand tile's scales for one step of a
+//      product are one 512-byte run.
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "nvfp4_device.hpp"
+
+namespace nvfp4 {
+
+// element types, as in nvfp4_dtype
+enum MxType { MX_F32 = 0, MX_BF16 = 1, MX_F16 = 2 };
+
+constexpr int kMxStep = 128;                // elements of K per scale word
+// workgroups of one launch, in one grid dimension
+constexpr int64_t kMxMaxGrid = (int64_t(1) << 31) - 1;
+
+// byte offset of the scale word of vector r, 128-element step kt
+__device__ __forceinline__ int64_t mx_sf_offset(int64_t r, int64_t kt, int64_t Kt) {
+    return (((r >> 7) * Kt + kt) * 128 + (r & 127)) * 4;
+}
+
+// E8M0 code of a block from the fp32 bits of its largest magnitude (sign
+// clear).  A subnormal or tiny maximum (biased exponent up to 2) gets code 0,
+// the least scale; an infinity or NaN makes the block NaN.
+__device__ __forceinline__ uint32_t mx_scale_code(uint32_t mag_bits) {
+    const uint32_t e = mag_bits >> 23;
+    return e == 255u ? 255u : (e > 2u ? e - 2u : 0u);
+}
+
+// The scale operand of gfx950's scaled conversions and MFMA is read as an
+// E8M0 exponent: bits c << 23 stand for 2^(c - 127), also for c = 0 (checked
+// for every bf16 and fp16 value under every code).  A NaN block's codes are
+// not defined; 254 keeps its conversions away from a NaN scale.
+__device__ __forceinline__ float mx_cvt_scale(uint32_t c) { return __uint_as_float((c < 254u ? c : 254u) << 23); }
+
+typedef __bf16 mx_bf16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 mx_f16x2 __attribute__((ext_vector_type(2)));
+
+// E2M1 codes of a pair of elements (raw: two 16-bit values, low half first)
+// under a scale, into byte SEL of `old`; the first in the low nibble
+template <int T, int SEL>
+__device__ __forceinline__ uint32_t mx_put16(uint32_t old, uint32_t raw, float scale) {
+    if constexpr (T == MX_BF16)
+        return __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(old, __builtin_bit_cast(mx_bf16x2, raw), scale, SEL);
+    else
+        return __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(old, __builtin_bit_cast(mx_f16x2, raw), scale, SEL);
+}
+template <int SEL>
+__device__ __forceinline__ uint32_t mx_put32(uint32_t old, uint32_t a, uint32_t b, float scale) {
+    return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(old, __uint_as_float(a), __uint_as_float(b), scale, SEL);
+}
+
+// magnitude bits of the element type -> fp32 magnitude bits
+template <int T>
+__device__ __forceinline__ uint32_t mx_mag_bits(uint32_t m) {
+    if constexpr (T == MX_F32) return m;
+    if constexpr (T == MX_BF16) return m << 16;
+    return __float_as_uint((float)__builtin_bit_cast(_Float16, (uint16_t)m));
+}
+
+// lane exchanges inside a row of 16 lanes
+template <int CTRL>
+__device__ __forceinline__ uint32_t mx_dpp(uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xf, 0xf, false);
+}
+constexpr int kDppXor1 = 0xB1, kDppXor2 = 0x4E;   // quad_perm [1,0,3,2] and [2,3,0,1]
+constexpr int kDppRor4 = 0x124, kDppRor8 = 0x128, kDppRor2 = 0x122, kDppRor1 = 0x121;
+
+// ------------------------------------------------------------------ groups
+//
+// The rows of group e are [offsets[e], offsets[e + 1]), in device memory; a
+// launch is sized by a bound on the number of tiles, and each workgroup finds
+// its own group.  Offsets are held to [0, R] and a group that would end before
+// it begins is empty, so no offset can lead outside a buffer.
+
+struct MxGroupTile {
+    int e;            // group, -1: past the last tile
+    int64_t begin;    // first row of the tile
+    int64_t end;      // end of the group's rows
+};
+
+__device__ __forceinline__ void mx_group_rows(const int32_t* offsets, int e, int64_t R, int64_t* begin, int64_t* end) {
+    int64_t a = offsets[e], b = offsets[e + 1];
+    a = a < 0 ? 0 : (a > R ? R : a);
+    b = b < a ? a : (b > R ? R : b);
+    *begin = a;
+    *end = b;
+}
+
+// The group of tile t when group e has cdiv(rows, unit) tiles, in order.
+// Called by whole waves; every lane gets the answer.  64 groups a step: an
+// inclusive scan over the lanes, then the first lane whose sum passes t.
+__device__ __forceinline__ MxGroupTile mx_find_group(const int32_t* __restrict__ offsets, int E, int64_t R,
+                                                     int unit, int64_t t) {
+    const int lane = (int)(threadIdx.x & 63);
+    int64_t base = 0;
+    for (int e0 = 0; e0 < E; e0 += 64) {
+        int64_t a = 0, b = 0;
+        if (e0 + lane < E) mx_group_rows(offsets, e0 + lane, R, &a, &b);
+        int n = (int)((b - a + unit - 1) / unit);
+        int s = n;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int v = __shfl_up(s, d, 64);
+            if (lane >= d) s += v;
+        }
+        const uint64_t past = __ballot(base + s > t);
+        if (past) {
+            const int l = __builtin_ctzll(past);
+            const int64_t ga = __shfl((long long)a, l, 64), gb = __shfl((long long)b, l, 64);
+            const int64_t first = base + __shfl(s - n, l, 64);
+            return MxGroupTile{e0 + l, ga + (t - first) * unit, gb};
+        }
+        base += __shfl(s, 63, 64);
+    }
+    return MxGroupTile{-1, 0, 0};
+}
+
+// tiles of `unit` rows that E groups of R rows can need at most
+inline int64_t mx_max_tiles(int64_t R, int64_t E, int64_t unit) {
+    const int64_t used = E < R ? E : R;
+    return (R + (unit - 1) * used) / unit;
+}
+
+// ----------------------------------------------------------------- launches
+
+struct MxCast {
+    const void* x;
+    int type;               // MxType
+    int64_t M, K, ldx;      // rows, columns and row pitch (elements) of x
+    const int32_t* rows;    // optional: vector r is x[rows[r]] (a row of zeros outside [0, M))
+    int64_t R;              // vectors (M without `rows`)
+    const int32_t* offsets; // optional: groups of vectors for the columnwise output
+    int E;
+    uint8_t *row_q, *row_sf, *col_q, *col_sf;
+};
+hipError_t launch_mx_cast(const MxCast& c, hipStream_t st);
+hipError_t launch_mx_dequant(const uint8_t* q, const uint8_t* sf, int64_t R, int64_t C, int type, void* out,
+                             hipStream_t st);
+
+struct MxGemm {
+    const uint8_t *a_q, *a_sf;   // [A][Kp/2]
+    int64_t A;                   // rows of a
+    const uint8_t *b_q, *b_sf;   // [N][Kp/2], or one such per group
+    int64_t M, N, Kp;            // M: rows of out
+    int type;                    // of out
+    void* out;
+    const int32_t* offsets;      // grouped: rows of out by group
+    int E;
+    const int32_t* rows;         // optional: row r of out is of a[rows[r]]
+    const float* row_scale;      // optional: factor of row r
+};
+hipError_t launch_mx_gemm(const MxGemm& g, hipStream_t st);
+
+struct MxWgrad {
+    const uint8_t *a_q, *a_sf;   // [N][Tp/2], a segment of 128-element steps per group
+    const uint8_t *b_q, *b_sf;   // [K][Tp/2]
+    int64_t N, K, Tp;
+    const int32_t* offsets;
+    int E;
+    int type;
+    void* out;                   // [E][N][K]
+};
+hipError_t launch_mx_wgrad(const MxWgrad& g, hipStream_t st);
+
+}  // namespace nvfp4

@@ -1,0 +1,255 @@
+// nvfp4_mx_api.cpp -- the C ABI of the MXFP4 cast and products (declared in
+// include/nvfp4.h): host-side validation, then stream-ordered launches.
+// Nothing is enqueued unless every check passes; the library allocates no
+// memory.
+#include <hip/hip_runtime.h>
+
+#include "nvfp4.h"
+#include "nvfp4_mx.hpp"
+#include "nvfp4_status.h"
+
+using namespace nvfp4;
+
+namespace {
+
+constexpr int64_t kMaxRows = (int64_t(1) << 31) - 1;   // rows and groups are 32-bit on the device
+constexpr int64_t kMaxK = int64_t(1) << 23;
+
+hipStream_t as_stream(void* s) { return reinterpret_cast<hipStream_t>(s); }
+int64_t up(int64_t n, int64_t m) { return (n + m - 1) / m * m; }
+int64_t type_size(int t) { return t == MX_F32 ? 4 : 2; }
+
+nvfp4_status check_type(int t, const char* name) {
+    if (t != MX_F32 && t != MX_BF16 && t != MX_F16) return fail(NVFP4_EINVAL, "unknown %s type %d", name, t);
+    return NVFP4_OK;
+}
+
+nvfp4_status check_count(int64_t n, int64_t most, const char* name) {
+    if (n < 0) return fail(NVFP4_EINVAL, "negative size %s=%lld", name, (long long)n);
+    if (n > most) return fail(NVFP4_ESHAPE, "%s must be at most %lld (%s=%lld)", name, (long long)most, name, (long long)n);
+    return NVFP4_OK;
+}
+
+nvfp4_status check_grid(int64_t a, int64_t b, const char* what) {
+    if (a > 0 && b > 0 && a > kMxMaxGrid / b) return fail(NVFP4_ESHAPE, "%s needs fewer than 2^31 tiles", what);
+    return NVFP4_OK;
+}
+
+// one operand's codes and scales
+nvfp4_status check_operand(const void* q, const void* sf, const char* name) {
+    if (!q || !sf) return fail(NVFP4_EINVAL, "%s: NULL argument", name);
+    if (!aligned(q, 16)) return fail(NVFP4_EALIGN, "%s_q must be 16-byte aligned", name);
+    if (!aligned(sf, 4)) return fail(NVFP4_EALIGN, "%s_sf must be 4-byte aligned", name);
+    return NVFP4_OK;
+}
+
+// one direction's outputs: both or neither
+nvfp4_status check_direction(const void* q, const void* sf, const char* name) {
+    if ((q != nullptr) != (sf != nullptr)) return fail(NVFP4_EINVAL, "%s output: q and sf must both be given (or both NULL)", name);
+    return q ? check_operand(q, sf, name) : NVFP4_OK;
+}
+
+nvfp4_status check_input(const void* x, int type, int64_t M, int64_t K, int64_t ldx) {
+    nvfp4_status s;
+    if ((s = check_type(type, "input")) != NVFP4_OK || (s = check_count(M, kMaxRows, "M")) != NVFP4_OK ||
+        (s = check_count(K, kMaxK, "K")) != NVFP4_OK)
+        return s;
+    if (ldx < 0 || ldx > (int64_t(1) << 40)) return fail(NVFP4_EINVAL, "row pitch ldx=%lld out of range", (long long)ldx);
+    if (M > 0 && K > 0 && !x) return fail(NVFP4_EINVAL, "x is NULL");
+    if (!aligned(x, (uintptr_t)type_size(type))) return fail(NVFP4_EALIGN, "x must be aligned to its type");
+    return NVFP4_OK;
+}
+
+nvfp4_status check_output(const void* out, int type) {
+    nvfp4_status s = check_type(type, "output");
+    if (s != NVFP4_OK) return s;
+    if (!out) return fail(NVFP4_EINVAL, "out is NULL");
+    if (!aligned(out, (uintptr_t)type_size(type))) return fail(NVFP4_EALIGN, "out must be aligned to its type");
+    return NVFP4_OK;
+}
+
+nvfp4_status check_groups(const int32_t* offsets, int32_t E, const int32_t* rows, const float* row_scale) {
+    if (E < 0) return fail(NVFP4_EINVAL, "num_groups < 0");
+    if (!offsets) return fail(NVFP4_EINVAL, "offsets is NULL");
+    if (!aligned(offsets, 4) || !aligned(rows, 4) || !aligned(row_scale, 4))
+        return fail(NVFP4_EALIGN, "offsets, rows and row_scale must be 4-byte aligned");
+    return NVFP4_OK;
+}
+
+nvfp4_status cast_impl(const void* x, int type, int64_t M, int64_t K, int64_t ldx, const int32_t* rows, int64_t R,
+                       const int32_t* offsets, int32_t E, uint8_t* row_q, uint8_t* row_sf, uint8_t* col_q,
+                       uint8_t* col_sf, void* stream) {
+    nvfp4_status s;
+    if ((s = check_input(x, type, M, K, ldx)) != NVFP4_OK || (s = check_count(R, kMaxRows, "R")) != NVFP4_OK ||
+        (s = check_direction(row_q, row_sf, "row")) != NVFP4_OK || (s = check_direction(col_q, col_sf, "col")) != NVFP4_OK)
+        return s;
+    if (!row_q && !col_q) return fail(NVFP4_EINVAL, "no output direction requested");
+    const int64_t tiles = offsets ? mx_max_tiles(R, E, 128) : up(R, 128) / 128;
+    if ((s = check_grid(2 * tiles + 2, up(K, 128) / 128, "cast")) != NVFP4_OK) return s;
+    if (R == 0 || K == 0 || (rows == nullptr && M == 0)) return ok();
+    const MxCast c{x, type, M, K, ldx, rows, R, offsets, E, row_q, row_sf, col_q, col_sf};
+    return (s = check_hip(launch_mx_cast(c, as_stream(stream)), "mx cast")) != NVFP4_OK ? s : ok();
+}
+
+nvfp4_status check_product(int64_t M, int64_t N, int64_t K) {
+    nvfp4_status s;
+    if ((s = check_count(M, kMaxRows, "M")) != NVFP4_OK || (s = check_count(N, kMaxRows, "N")) != NVFP4_OK ||
+        (s = check_count(K, kMaxK, "K")) != NVFP4_OK)
+        return s;
+    return NVFP4_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+nvfp4_status nvfp4_mx_quantize(const void* x, nvfp4_dtype type, int64_t M, int64_t K, int64_t ldx, uint8_t* row_q,
+                               uint8_t* row_sf, uint8_t* col_q, uint8_t* col_sf, void* stream) {
+    return cast_impl(x, type, M, K, ldx, nullptr, M, nullptr, 0, row_q, row_sf, col_q, col_sf, stream);
+}
+
+nvfp4_status nvfp4_mx_quantize_grouped(const void* x, nvfp4_dtype type, int64_t M, int64_t K, int64_t ldx,
+                                       const int32_t* rows, int64_t R, const int32_t* offsets, int32_t num_groups,
+                                       uint8_t* row_q, uint8_t* row_sf, uint8_t* col_q, uint8_t* col_sf, void* stream) {
+    nvfp4_status s = check_groups(offsets, num_groups, rows, nullptr);
+    if (s != NVFP4_OK) return s;
+    if (!rows && R != M) return fail(NVFP4_EINVAL, "without rows R must be M (R=%lld, M=%lld)", (long long)R, (long long)M);
+    return cast_impl(x, type, M, K, ldx, rows, R, offsets, num_groups, row_q, row_sf, col_q, col_sf, stream);
+}
+
+nvfp4_status nvfp4_mx_dequantize(const uint8_t* q, const uint8_t* sf, int64_t R, int64_t C, nvfp4_dtype out_type,
+                                 void* out, void* stream) {
+    nvfp4_status s;
+    if ((s = check_type(out_type, "output")) != NVFP4_OK || (s = check_count(R, kMaxRows, "R")) != NVFP4_OK ||
+        (s = check_count(C, kMaxRows, "C")) != NVFP4_OK)
+        return s;
+    if (R == 0 || C == 0) return ok();
+    if ((s = check_operand(q, sf, "mx")) != NVFP4_OK || (s = check_output(out, out_type)) != NVFP4_OK) return s;
+    return (s = check_hip(launch_mx_dequant(q, sf, R, C, out_type, out, as_stream(stream)), "mx dequantize")) != NVFP4_OK
+               ? s
+               : ok();
+}
+
+nvfp4_status nvfp4_mx_gemm(const uint8_t* a_q, const uint8_t* a_sf, const uint8_t* b_q, const uint8_t* b_sf, int64_t M,
+                           int64_t N, int64_t K, nvfp4_dtype out_type, void* out, void* stream) {
+    nvfp4_status s;
+    if ((s = check_type(out_type, "output")) != NVFP4_OK || (s = check_product(M, N, K)) != NVFP4_OK) return s;
+    if (M == 0 || N == 0) return ok();
+    if ((s = check_grid(up(M, 128) / 128, up(N, 128) / 128, "mx gemm")) != NVFP4_OK ||
+        (s = check_output(out, out_type)) != NVFP4_OK)
+        return s;
+    if (K > 0 && ((s = check_operand(a_q, a_sf, "a")) != NVFP4_OK || (s = check_operand(b_q, b_sf, "b")) != NVFP4_OK))
+        return s;
+    const MxGemm g{a_q, a_sf, M, b_q, b_sf, M, N, up(K, 128), out_type, out, nullptr, 0, nullptr, nullptr};
+    return (s = check_hip(launch_mx_gemm(g, as_stream(stream)), "mx gemm")) != NVFP4_OK ? s : ok();
+}
+
+nvfp4_status nvfp4_mx_gemm_grouped(const uint8_t* a_q, const uint8_t* a_sf, int64_t A, const int32_t* rows, int64_t R,
+                                   const int32_t* offsets, int32_t num_groups, const uint8_t* b_q, const uint8_t* b_sf,
+                                   int64_t N, int64_t K, const float* row_scale, nvfp4_dtype out_type, void* out,
+                                   void* stream) {
+    nvfp4_status s;
+    if ((s = check_groups(offsets, num_groups, rows, row_scale)) != NVFP4_OK ||
+        (s = check_type(out_type, "output")) != NVFP4_OK || (s = check_product(R, N, K)) != NVFP4_OK ||
+        (s = check_count(A, kMaxRows, "A")) != NVFP4_OK)
+        return s;
+    if (!rows && R != A) return fail(NVFP4_EINVAL, "without rows R must be A (R=%lld, A=%lld)", (long long)R, (long long)A);
+    if (R == 0 || N == 0 || num_groups == 0) return ok();
+    if (A == 0) return fail(NVFP4_EINVAL, "rows of an empty operand (A=0, R=%lld)", (long long)R);
+    if ((s = check_grid(mx_max_tiles(R, num_groups, 128), up(N, 128) / 128, "mx gemm")) != NVFP4_OK ||
+        (s = check_output(out, out_type)) != NVFP4_OK)
+        return s;
+    if (K > 0 && ((s = check_operand(a_q, a_sf, "a")) != NVFP4_OK || (s = check_operand(b_q, b_sf, "b")) != NVFP4_OK))
+        return s;
+    const MxGemm g{a_q, a_sf, A, b_q, b_sf, R, N, up(K, 128), out_type, out, offsets, num_groups, rows, row_scale};
+    return (s = check_hip(launch_mx_gemm(g, as_stream(stream)), "mx grouped gemm")) != NVFP4_OK ? s : ok();
+}
+
+nvfp4_status nvfp4_mx_wgrad_grouped(const uint8_t* a_q, const uint8_t* a_sf, const uint8_t* b_q, const uint8_t* b_sf,
+                                    int64_t N, int64_t K, int64_t Tp, const int32_t* offsets, int32_t num_groups,
+                                    nvfp4_dtype out_type, void* out, void* stream) {
+    nvfp4_status s;
+    if ((s = check_groups(offsets, num_groups, nullptr, nullptr)) != NVFP4_OK ||
+        (s = check_type(out_type, "output")) != NVFP4_OK || (s = check_count(N, kMaxRows, "N")) != NVFP4_OK ||
+        (s = check_count(K, kMaxRows, "K")) != NVFP4_OK || (s = check_count(Tp, 2 * kMaxRows, "Tp")) != NVFP4_OK)
+        return s;
+    if (Tp % 128 != 0) return fail(NVFP4_ESHAPE, "Tp must be a multiple of 128 (Tp=%lld)", (long long)Tp);
+    if (N == 0 || K == 0 || num_groups == 0) return ok();
+    if ((s = check_grid(up(N, 128) / 128, up(K, 128) / 128, "mx wgrad")) != NVFP4_OK ||
+        (s = check_grid(up(N, 128) / 128 * (up(K, 128) / 128), num_groups, "mx wgrad")) != NVFP4_OK ||
+        (s = check_output(out, out_type)) != NVFP4_OK)
+        return s;
+    if (Tp > 0 && ((s = check_operand(a_q, a_sf, "a")) != NVFP4_OK || (s = check_operand(b_q, b_sf, "b")) != NVFP4_OK))
+        return s;
+    const MxWgrad g{a_q, a_sf, b_q, b_sf, N, K, Tp, offsets, num_groups, out_type, out};
+    return (s = check_hip(launch_mx_wgrad(g, as_stream(stream)), "mx wgrad")) != NVFP4_OK ? s : ok();
+}
+
+int64_t nvfp4_mx_linear_workspace(int64_t M, int64_t N, int64_t K) {
+    if (M < 0 || N < 0 || K < 0 || M > kMaxRows || N > kMaxRows || K > kMaxK) return 0;
+    return M * (up(K, 128) / 2) + up(M, 128) * (up(K, 128) / 32);
+}
+
+nvfp4_status nvfp4_mx_linear(const void* x, nvfp4_dtype x_type, int64_t M, int64_t K, int64_t ldx, const uint8_t* w_q,
+                             const uint8_t* w_sf, int64_t N, nvfp4_dtype out_type, void* out, void* workspace,
+                             int64_t workspace_bytes, void* stream) {
+    nvfp4_status s;
+    if ((s = check_input(x, x_type, M, K, ldx)) != NVFP4_OK || (s = check_type(out_type, "output")) != NVFP4_OK ||
+        (s = check_product(M, N, K)) != NVFP4_OK)
+        return s;
+    if (M == 0 || N == 0) return ok();
+    if ((s = check_grid(up(M, 128) / 128, up(N, 128) / 128, "mx linear")) != NVFP4_OK ||
+        (s = check_output(out, out_type)) != NVFP4_OK)
+        return s;
+    if (K > 0 && (s = check_operand(w_q, w_sf, "w")) != NVFP4_OK) return s;
+    const int64_t need = nvfp4_mx_linear_workspace(M, N, K);
+    if (need > 0 && (!workspace || workspace_bytes < need))
+        return fail(NVFP4_EINVAL, "workspace of %lld bytes needed", (long long)need);
+    if (!aligned(workspace, 16)) return fail(NVFP4_EALIGN, "workspace must be 16-byte aligned");
+    uint8_t* q = (uint8_t*)workspace;
+    uint8_t* sf = q + M * (up(K, 128) / 2);
+    if (K > 0) {
+        const MxCast c{x, x_type, M, K, ldx, nullptr, M, nullptr, 0, q, sf, nullptr, nullptr};
+        if ((s = check_hip(launch_mx_cast(c, as_stream(stream)), "mx cast")) != NVFP4_OK) return s;
+    }
+    const MxGemm g{q, sf, M, w_q, w_sf, M, N, up(K, 128), out_type, out, nullptr, 0, nullptr, nullptr};
+    return (s = check_hip(launch_mx_gemm(g, as_stream(stream)), "mx gemm")) != NVFP4_OK ? s : ok();
+}
+
+int64_t nvfp4_mx_linear_grouped_workspace(int64_t M, int64_t R, int64_t N, int64_t K) {
+    (void)R;
+    return nvfp4_mx_linear_workspace(M, N, K);
+}
+
+nvfp4_status nvfp4_mx_linear_grouped(const void* x, nvfp4_dtype x_type, int64_t M, int64_t K, int64_t ldx,
+                                     const int32_t* rows, int64_t R, const int32_t* offsets, int32_t num_groups,
+                                     const uint8_t* w_q, const uint8_t* w_sf, int64_t N, const float* row_scale,
+                                     nvfp4_dtype out_type, void* out, void* workspace, int64_t workspace_bytes,
+                                     void* stream) {
+    nvfp4_status s;
+    if ((s = check_groups(offsets, num_groups, rows, row_scale)) != NVFP4_OK ||
+        (s = check_input(x, x_type, M, K, ldx)) != NVFP4_OK || (s = check_type(out_type, "output")) != NVFP4_OK ||
+        (s = check_product(R, N, K)) != NVFP4_OK)
+        return s;
+    if (!rows && R != M) return fail(NVFP4_EINVAL, "without rows R must be M (R=%lld, M=%lld)", (long long)R, (long long)M);
+    if (R == 0 || N == 0 || num_groups == 0) return ok();
+    if (M == 0) return fail(NVFP4_EINVAL, "rows of an empty x (M=0, R=%lld)", (long long)R);
+    if ((s = check_grid(mx_max_tiles(R, num_groups, 128), up(N, 128) / 128, "mx linear")) != NVFP4_OK ||
+        (s = check_output(out, out_type)) != NVFP4_OK)
+        return s;
+    if (K > 0 && (s = check_operand(w_q, w_sf, "w")) != NVFP4_OK) return s;
+    const int64_t need = nvfp4_mx_linear_grouped_workspace(M, R, N, K);
+    if (need > 0 && (!workspace || workspace_bytes < need))
+        return fail(NVFP4_EINVAL, "workspace of %lld bytes needed", (long long)need);
+    if (!aligned(workspace, 16)) return fail(NVFP4_EALIGN, "workspace must be 16-byte aligned");
+    uint8_t* q = (uint8_t*)workspace;
+    uint8_t* sf = q + M * (up(K, 128) / 2);
+    if (K > 0) {
+        const MxCast c{x, x_type, M, K, ldx, nullptr, M, nullptr, 0, q, sf, nullptr, nullptr};
+        if ((s = check_hip(launch_mx_cast(c, as_stream(stream)), "mx cast")) != NVFP4_OK) return s;
+    }
+    const MxGemm g{q, sf, M, w_q, w_sf, R, N, up(K, 128), out_type, out, offsets, num_groups, rows, row_scale};
+    return (s = check_hip(launch_mx_gemm(g, as_stream(stream)), "mx grouped gemm")) != NVFP4_OK ? s : ok();
+}
+
+}  // extern "C"

@@ -1,0 +1,414 @@
+// nvfp4_mx_cast.hip -- the MXFP4 cast and dequantization for gfx950
+// (arithmetic and layout: nvfp4_mx.hpp).
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "nvfp4_mx.hpp"
+
+namespace nvfp4 {
+namespace {
+
+// ------------------------------------------------------------- rowwise only
+//
+// A wave takes 16 rows by 512 columns: 8 elements a lane, one 1-KiB (2-byte
+// types) run of a row per load.  Four lanes share a block: its maximum takes
+// two lane exchanges, and a lane's 8 codes are one word of the output.  A
+// 16-lane group holds the four scales of one 128-element step; lane i of it
+// keeps the word of row i, so the 16 rows' words leave in one store.
+constexpr int kRowsPerWave = 16, kRowCols = 512;
+
+template <int T>
+struct Eight {                       // 8 elements of one row
+    uint32_t w[T == MX_F32 ? 8 : 4];
+};
+
+template <int T>
+__device__ __forceinline__ Eight<T> load_eight(const char* p, int valid) {
+    constexpr int B = T == MX_F32 ? 4 : 2;
+    Eight<T> v;
+    if (valid >= 8) {
+        __builtin_memcpy(&v, p, sizeof v);   // any alignment: the hardware splits what it has to
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8 * B / 4; ++i) {
+            if constexpr (T == MX_F32) {
+                v.w[i] = i < valid ? *(const uint32_t*)(p + 4 * i) : 0u;
+            } else {
+                const uint32_t lo = 2 * i < valid ? *(const uint16_t*)(p + 4 * i) : 0u;
+                const uint32_t hi = 2 * i + 1 < valid ? *(const uint16_t*)(p + 4 * i + 2) : 0u;
+                v.w[i] = lo | hi << 16;
+            }
+        }
+    }
+    return v;
+}
+
+template <int T>
+__device__ __forceinline__ uint32_t eight_mag(const Eight<T>& v) {
+    if constexpr (T == MX_F32) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t a = v.w[i] & 0x7fffffffu;
+            m = a > m ? a : m;
+        }
+        return m;
+    } else {
+        return max_halves(pk_max_u16(pk_max_u16(abs2(v.w[0]), abs2(v.w[1])), pk_max_u16(abs2(v.w[2]), abs2(v.w[3]))));
+    }
+}
+
+template <int T>
+__device__ __forceinline__ uint32_t eight_codes(const Eight<T>& v, float scale) {
+    if constexpr (T == MX_F32) {
+        uint32_t q = mx_put32<0>(0u, v.w[0], v.w[1], scale);
+        q = mx_put32<1>(q, v.w[2], v.w[3], scale);
+        q = mx_put32<2>(q, v.w[4], v.w[5], scale);
+        return mx_put32<3>(q, v.w[6], v.w[7], scale);
+    } else {
+        uint32_t q = mx_put16<T, 0>(0u, v.w[0], scale);
+        q = mx_put16<T, 1>(q, v.w[1], scale);
+        q = mx_put16<T, 2>(q, v.w[2], scale);
+        return mx_put16<T, 3>(q, v.w[3], scale);
+    }
+}
+
+template <int T, bool GATHER>
+__global__ __launch_bounds__(256) void k_mx_rows(MxCast c, uint32_t nchunk) {
+    constexpr int B = T == MX_F32 ? 4 : 2;
+    const int lane = (int)(threadIdx.x & 63), wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    const int64_t r0 = ((int64_t)(blockIdx.x / nchunk) * 4 + wave) * kRowsPerWave;
+    const int64_t c0 = (int64_t)(blockIdx.x % nchunk) * kRowCols + 8 * lane;
+    const int64_t Kt = (c.K + kMxStep - 1) / kMxStep;
+    const int64_t left = c.K - c0;
+    const int valid = left >= 8 ? 8 : (left > 0 ? (int)left : 0);
+    const int64_t kb = c0 / kMxStep;
+    int idx = 0;
+    if constexpr (GATHER) idx = r0 + (lane & 15) < c.R ? c.rows[r0 + (lane & 15)] : -1;
+    uint32_t keep = 0;
+#pragma unroll 4
+    for (int i = 0; i < kRowsPerWave; ++i) {
+        const int64_t r = r0 + i;
+        int64_t src = r;
+        if constexpr (GATHER) src = __builtin_amdgcn_readlane(idx, i);
+        const bool have = r < c.R && src >= 0 && src < c.M;
+        const Eight<T> v = load_eight<T>((const char*)c.x + (src * c.ldx + c0) * B, have ? valid : 0);
+        uint32_t m = eight_mag<T>(v), o;
+        o = mx_dpp<kDppXor1>(m);
+        m = o > m ? o : m;
+        o = mx_dpp<kDppXor2>(m);
+        m = o > m ? o : m;
+        const uint32_t code = mx_scale_code(mx_mag_bits<T>(m));
+        const uint32_t q = eight_codes<T>(v, mx_cvt_scale(code));
+        if (r < c.R && kb < Kt) *(uint32_t*)(c.row_q + r * (Kt * (kMxStep / 2)) + c0 / 2) = q;
+        uint32_t word = code << (8 * ((lane >> 2) & 3));
+        word |= mx_dpp<kDppRor4>(word);
+        word |= mx_dpp<kDppRor8>(word);
+        keep = (lane & 15) == i ? word : keep;
+    }
+    // rows past R, up to the 128-row tile's end: scale code 0
+    const int64_t r = r0 + (lane & 15);
+    if (kb < Kt && r < (c.R + 127) / 128 * 128) *(uint32_t*)(c.row_sf + mx_sf_offset(r, kb, Kt)) = keep;
+}
+
+// --------------------------------------------------------- both directions
+//
+// A workgroup takes a 128 x 128 tile, which is one 512-byte scale tile of
+// either direction, so x is read once.  Wave w has rows 32 w .. 32 w + 31 and
+// a lane two adjacent columns: a column's block of 32 rows is within the lane
+// (its maximum and its 16 code bytes need no exchange), and a row's block of
+// 32 columns is 16 lanes, whose maximum is four rotations inside a DPP row.
+// Codes go through LDS only to leave in whole 64-byte runs.
+template <int T>
+struct Two {
+    uint32_t w[T == MX_F32 ? 2 : 1];
+};
+
+template <int T>
+__device__ __forceinline__ Two<T> load_two(const char* p, int valid) {
+    Two<T> v;
+    if (valid >= 2) {
+        __builtin_memcpy(&v, p, sizeof v);
+    } else if constexpr (T == MX_F32) {
+        v.w[0] = valid > 0 ? *(const uint32_t*)p : 0u;
+        v.w[1] = 0u;
+    } else {
+        v.w[0] = valid > 0 ? *(const uint16_t*)p : 0u;
+    }
+    return v;
+}
+
+template <int T>
+__device__ __forceinline__ uint32_t two_mag(const Two<T>& v) {
+    if constexpr (T == MX_F32) {
+        const uint32_t a = v.w[0] & 0x7fffffffu, b = v.w[1] & 0x7fffffffu;
+        return a > b ? a : b;
+    } else {
+        return max_halves(abs2(v.w[0]));
+    }
+}
+
+template <int T, int SEL>
+__device__ __forceinline__ uint32_t put_row(uint32_t old, const Two<T>& v, float scale) {
+    if constexpr (T == MX_F32) return mx_put32<SEL>(old, v.w[0], v.w[1], scale);
+    else return mx_put16<T, SEL>(old, v.w[0], scale);
+}
+
+// column COL (0 or 1) of rows a and b
+template <int T, int SEL, int COL>
+__device__ __forceinline__ uint32_t put_col(uint32_t old, const Two<T>& a, const Two<T>& b, float scale) {
+    if constexpr (T == MX_F32) return mx_put32<SEL>(old, a.w[COL], b.w[COL], scale);
+    else return mx_put16<T, SEL>(old, __builtin_amdgcn_perm(b.w[0], a.w[0], COL ? 0x07060302u : 0x05040100u), scale);
+}
+
+constexpr int kColPitch = 20;   // words per column's 64 code bytes in LDS: 16-byte aligned, off the banks' period
+
+struct TileLds {
+    uint32_t colq[128 * kColPitch];
+    uint32_t rowq[4][8][64];      // [wave][rows 4 g .. 4 g + 3][lane]: one byte per row
+    uint8_t rsf[128][4];
+    uint8_t csf[128][4];
+};
+
+// bytes j of four words -> word j (a 4 x 4 byte transpose)
+__device__ __forceinline__ void transpose4(const uint32_t* w, uint32_t* o) {
+    const uint32_t a = __builtin_amdgcn_perm(w[1], w[0], 0x05010400u), b = __builtin_amdgcn_perm(w[1], w[0], 0x07030602u);
+    const uint32_t c = __builtin_amdgcn_perm(w[3], w[2], 0x05010400u), d = __builtin_amdgcn_perm(w[3], w[2], 0x07030602u);
+    o[0] = __builtin_amdgcn_perm(c, a, 0x05040100u);
+    o[1] = __builtin_amdgcn_perm(c, a, 0x07060302u);
+    o[2] = __builtin_amdgcn_perm(d, b, 0x05040100u);
+    o[3] = __builtin_amdgcn_perm(d, b, 0x07060302u);
+}
+
+template <int T, bool ROW, bool GROUPED>
+__global__ __launch_bounds__(256) void k_mx_tile(MxCast c, uint32_t nkt, int64_t Tt) {
+    constexpr int B = T == MX_F32 ? 4 : 2;
+    __shared__ __attribute__((aligned(16))) TileLds S;
+    const int tid = (int)threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int64_t mt = blockIdx.x / nkt, kt = blockIdx.x % nkt;
+    int64_t r0 = mt * 128, rend = c.R;
+    if constexpr (GROUPED) {
+        const MxGroupTile g = mx_find_group(c.offsets, c.E, c.R, 128, mt);
+        if (g.e < 0) return;
+        r0 = g.begin;
+        rend = g.end;
+    }
+    const int nrow = (int)(rend - r0 < 128 ? rend - r0 : 128);   // >= 1
+    const int64_t c0 = kt * 128 + 2 * lane, left = c.K - c0;
+    const int valid = left >= 2 ? 2 : (left > 0 ? 1 : 0);
+
+    Two<T> v[32];
+    int idx = 0;
+    if (c.rows) idx = 32 * wave + (lane & 31) < nrow ? c.rows[r0 + 32 * wave + (lane & 31)] : -1;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+        int64_t src = r0 + 32 * wave + i;
+        if (c.rows) src = __builtin_amdgcn_readlane(idx, i);
+        const bool have = 32 * wave + i < nrow && src >= 0 && src < c.M;
+        v[i] = load_two<T>((const char*)c.x + (src * c.ldx + c0) * B, have ? valid : 0);
+    }
+
+    // columns: this wave's 32 rows are one block of each of the lane's two
+    uint32_t m0 = 0, m1 = 0;
+    if constexpr (T == MX_F32) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+            const uint32_t a = v[i].w[0] & 0x7fffffffu, b = v[i].w[1] & 0x7fffffffu;
+            m0 = a > m0 ? a : m0;
+            m1 = b > m1 ? b : m1;
+        }
+    } else {
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) m = pk_max_u16(m, abs2(v[i].w[0]));
+        m0 = m & 0xffffu;
+        m1 = m >> 16;
+    }
+    {
+        const uint32_t k0 = mx_scale_code(mx_mag_bits<T>(m0)), k1 = mx_scale_code(mx_mag_bits<T>(m1));
+        const float s0 = mx_cvt_scale(k0), s1 = mx_cvt_scale(k1);
+        u32x4 q0, q1;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            uint32_t a = put_col<T, 0, 0>(0u, v[8 * j], v[8 * j + 1], s0);
+            a = put_col<T, 1, 0>(a, v[8 * j + 2], v[8 * j + 3], s0);
+            a = put_col<T, 2, 0>(a, v[8 * j + 4], v[8 * j + 5], s0);
+            q0[j] = put_col<T, 3, 0>(a, v[8 * j + 6], v[8 * j + 7], s0);
+            uint32_t b = put_col<T, 0, 1>(0u, v[8 * j], v[8 * j + 1], s1);
+            b = put_col<T, 1, 1>(b, v[8 * j + 2], v[8 * j + 3], s1);
+            b = put_col<T, 2, 1>(b, v[8 * j + 4], v[8 * j + 5], s1);
+            q1[j] = put_col<T, 3, 1>(b, v[8 * j + 6], v[8 * j + 7], s1);
+        }
+        *(u32x4*)&S.colq[(2 * lane) * kColPitch + 4 * wave] = q0;
+        *(u32x4*)&S.colq[(2 * lane + 1) * kColPitch + 4 * wave] = q1;
+        S.csf[2 * lane][wave] = (uint8_t)k0;
+        S.csf[2 * lane + 1][wave] = (uint8_t)k1;
+    }
+
+    if constexpr (ROW) {
+        uint32_t keep0 = 0, keep1 = 0;
+#pragma unroll
+        for (int g = 0; g < 8; ++g) {
+            uint32_t code[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int i = 4 * g + j;
+                uint32_t m = two_mag<T>(v[i]), o;
+                o = mx_dpp<kDppRor8>(m);
+                m = o > m ? o : m;
+                o = mx_dpp<kDppRor4>(m);
+                m = o > m ? o : m;
+                o = mx_dpp<kDppRor2>(m);
+                m = o > m ? o : m;
+                o = mx_dpp<kDppRor1>(m);
+                m = o > m ? o : m;
+                code[j] = mx_scale_code(mx_mag_bits<T>(m));
+                if (i < 16) keep0 = (lane & 15) == i ? code[j] : keep0;
+                else keep1 = (lane & 15) == i - 16 ? code[j] : keep1;
+            }
+            uint32_t q = put_row<T, 0>(0u, v[4 * g], mx_cvt_scale(code[0]));
+            q = put_row<T, 1>(q, v[4 * g + 1], mx_cvt_scale(code[1]));
+            q = put_row<T, 2>(q, v[4 * g + 2], mx_cvt_scale(code[2]));
+            S.rowq[wave][g][lane] = put_row<T, 3>(q, v[4 * g + 3], mx_cvt_scale(code[3]));
+        }
+        S.rsf[32 * wave + (lane & 15)][lane >> 4] = (uint8_t)keep0;
+        S.rsf[32 * wave + 16 + (lane & 15)][lane >> 4] = (uint8_t)keep1;
+    }
+    __syncthreads();
+
+    if (c.col_q) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int id = tid + 256 * j, col = id >> 2, part = id & 3;
+            if (kt * 128 + col < c.K)
+                *(u32x4*)(c.col_q + ((kt * 128 + col) * Tt + mt) * 64 + 16 * part) = *(const u32x4*)&S.colq[col * kColPitch + 4 * part];
+        }
+        if (tid < 128) *(uint32_t*)(c.col_sf + ((kt * Tt + mt) * 128 + tid) * 4) = *(const uint32_t*)S.csf[tid];
+    }
+    if constexpr (ROW) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int id = tid + 256 * j, w = id >> 7, g = (id >> 4) & 7, p = id & 15;
+            const u32x4 in = *(const u32x4*)&S.rowq[w][g][4 * p];
+            const uint32_t a[4] = {in.x, in.y, in.z, in.w};
+            uint32_t o[4];
+            transpose4(a, o);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int row = 32 * w + 4 * g + i;
+                if (row < nrow) *(uint32_t*)(c.row_q + ((r0 + row) * nkt + kt) * 64 + 4 * p) = o[i];
+            }
+        }
+        // without groups the tile's rows are a whole scale tile, codes past R are 0
+        if (tid < (GROUPED ? nrow : 128))
+            *(uint32_t*)(c.row_sf + mx_sf_offset(r0 + tid, kt, nkt)) = *(const uint32_t*)S.rsf[tid];
+    }
+}
+
+// ------------------------------------------------------------- dequantize
+
+// fp32 value of a scale code; code 0's is subnormal in fp32, 255 is NaN
+__device__ __forceinline__ float scale_value(uint32_t c) {
+    return c == 255u ? __uint_as_float(0x7fc00000u) : (c ? __uint_as_float(c << 23) : 0x1p-127f);
+}
+
+// A thread takes 8 elements: one word of codes, 16 or 32 bytes out.  Grid
+// magnitude times a power of two is exact in fp32 except below 2^-149, which
+// no code reaches (0.5 * 2^-127 = 2^-128).
+template <int T>
+__global__ __launch_bounds__(256) void k_mx_dequant(const uint8_t* __restrict__ q, const uint8_t* __restrict__ sf,
+                                                    int64_t R, int64_t C, char* __restrict__ out) {
+    const int64_t per = (C + 7) / 8, n = R * per, Kt = (C + kMxStep - 1) / kMxStep;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+        const int64_t r = i / per, c0 = (i - r * per) * 8;
+        const uint32_t w = *(const uint32_t*)(q + r * (Kt * 64) + c0 / 2);
+        const float s = scale_value(sf[mx_sf_offset(r, c0 >> 7, Kt) + ((c0 >> 5) & 3)]);
+        float v[8];
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            typedef float f32x2 __attribute__((ext_vector_type(2)));
+            f32x2 g;
+            if (b == 0) g = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 0);
+            else if (b == 1) g = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 1);
+            else if (b == 2) g = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 2);
+            else g = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 3);
+            v[2 * b] = g.x * s;
+            v[2 * b + 1] = g.y * s;
+        }
+        const int64_t left = C - c0;
+        if constexpr (T == MX_F32) {
+            char* o = out + (r * C + c0) * 4;
+            if (left >= 8) {
+                __builtin_memcpy(o, v, 32);
+            } else {
+                for (int k = 0; k < (int)left; ++k) ((float*)o)[k] = v[k];
+            }
+        } else {
+            uint32_t p[4];
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                if constexpr (T == MX_BF16) {
+                    p[b] = bf16x2_rne(v[2 * b], v[2 * b + 1]);
+                } else {
+                    const mx_f16x2 h = {(_Float16)v[2 * b], (_Float16)v[2 * b + 1]};
+                    p[b] = __builtin_bit_cast(uint32_t, h);
+                }
+            }
+            char* o = out + (r * C + c0) * 2;
+            if (left >= 8) {
+                __builtin_memcpy(o, p, 16);
+            } else {
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    if (k < left) ((uint16_t*)o)[k] = (uint16_t)(p[k >> 1] >> (16 * (k & 1)));
+            }
+        }
+    }
+}
+
+template <int T>
+hipError_t launch_cast(const MxCast& c, hipStream_t st) {
+    const int64_t Kt = (c.K + kMxStep - 1) / kMxStep;
+    if (!c.col_q) {
+        const int64_t chunks = (c.K + kRowCols - 1) / kRowCols, groups = (c.R + 127) / 128 * (128 / (4 * kRowsPerWave));
+        if (chunks * groups > kMxMaxGrid) return hipErrorInvalidValue;
+        const dim3 grid((unsigned)(chunks * groups));
+        if (c.rows) k_mx_rows<T, true><<<grid, 256, 0, st>>>(c, (uint32_t)chunks);
+        else k_mx_rows<T, false><<<grid, 256, 0, st>>>(c, (uint32_t)chunks);
+        return hipGetLastError();
+    }
+    const int64_t Tt = c.offsets ? mx_max_tiles(c.R, c.E, 128) : (c.R + 127) / 128;
+    if (Tt * Kt > kMxMaxGrid) return hipErrorInvalidValue;
+    const dim3 grid((unsigned)(Tt * Kt));
+    const uint32_t nkt = (uint32_t)Kt;
+    if (c.offsets) {
+        if (c.row_q) k_mx_tile<T, true, true><<<grid, 256, 0, st>>>(c, nkt, Tt);
+        else k_mx_tile<T, false, true><<<grid, 256, 0, st>>>(c, nkt, Tt);
+    } else {
+        if (c.row_q) k_mx_tile<T, true, false><<<grid, 256, 0, st>>>(c, nkt, Tt);
+        else k_mx_tile<T, false, false><<<grid, 256, 0, st>>>(c, nkt, Tt);
+    }
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_mx_cast(const MxCast& c, hipStream_t st) {
+    if (c.R <= 0 || c.K <= 0) return hipSuccess;
+    if (c.type == MX_F32) return launch_cast<MX_F32>(c, st);
+    if (c.type == MX_BF16) return launch_cast<MX_BF16>(c, st);
+    return launch_cast<MX_F16>(c, st);
+}
+
+hipError_t launch_mx_dequant(const uint8_t* q, const uint8_t* sf, int64_t R, int64_t C, int type, void* out,
+                             hipStream_t st) {
+    if (R <= 0 || C <= 0) return hipSuccess;
+    const int64_t blocks = (R * ((C + 7) / 8) + 255) / 256;
+    const dim3 grid((unsigned)(blocks < 256 * 1024 ? blocks : 256 * 1024));
+    if (type == MX_F32) k_mx_dequant<MX_F32><<<grid, 256, 0, st>>>(q, sf, R, C, (char*)out);
+    else if (type == MX_BF16) k_mx_dequant<MX_BF16><<<grid, 256, 0, st>>>(q, sf, R, C, (char*)out);
+    else k_mx_dequant<MX_F16><<<grid, 256, 0, st>>>(q, sf, R, C, (char*)out);
+    return hipGetLastError();
+}
+
+}  // namespace nvfp4
