@@ -75,6 +75,64 @@ __device__ __forceinline__ uint32_t mx_mag_bits(uint32_t m) {
     return __float_as_uint((float)__builtin_bit_cast(_Float16, (uint16_t)m));
 }
 
+// 8 elements of one vector, 16 or 32 bytes: loaded, their largest magnitude
+// (bits of their type) and their codes under a scale
+template <int T>
+struct Eight {                       // 8 elements of one row
+    uint32_t w[T == MX_F32 ? 8 : 4];
+};
+
+template <int T>
+__device__ __forceinline__ Eight<T> load_eight(const char* p, int valid) {
+    constexpr int B = T == MX_F32 ? 4 : 2;
+    Eight<T> v;
+    if (valid >= 8) {
+        __builtin_memcpy(&v, p, sizeof v);   // any alignment: the hardware splits what it has to
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8 * B / 4; ++i) {
+            if constexpr (T == MX_F32) {
+                v.w[i] = i < valid ? *(const uint32_t*)(p + 4 * i) : 0u;
+            } else {
+                const uint32_t lo = 2 * i < valid ? *(const uint16_t*)(p + 4 * i) : 0u;
+                const uint32_t hi = 2 * i + 1 < valid ? *(const uint16_t*)(p + 4 * i + 2) : 0u;
+                v.w[i] = lo | hi << 16;
+            }
+        }
+    }
+    return v;
+}
+
+template <int T>
+__device__ __forceinline__ uint32_t eight_mag(const Eight<T>& v) {
+    if constexpr (T == MX_F32) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t a = v.w[i] & 0x7fffffffu;
+            m = a > m ? a : m;
+        }
+        return m;
+    } else {
+        return max_halves(pk_max_u16(pk_max_u16(abs2(v.w[0]), abs2(v.w[1])), pk_max_u16(abs2(v.w[2]), abs2(v.w[3]))));
+    }
+}
+
+template <int T>
+__device__ __forceinline__ uint32_t eight_codes(const Eight<T>& v, float scale) {
+    if constexpr (T == MX_F32) {
+        uint32_t q = mx_put32<0>(0u, v.w[0], v.w[1], scale);
+        q = mx_put32<1>(q, v.w[2], v.w[3], scale);
+        q = mx_put32<2>(q, v.w[4], v.w[5], scale);
+        return mx_put32<3>(q, v.w[6], v.w[7], scale);
+    } else {
+        uint32_t q = mx_put16<T, 0>(0u, v.w[0], scale);
+        q = mx_put16<T, 1>(q, v.w[1], scale);
+        q = mx_put16<T, 2>(q, v.w[2], scale);
+        return mx_put16<T, 3>(q, v.w[3], scale);
+    }
+}
+
 // lane exchanges inside a row of 16 lanes
 template <int CTRL>
 __device__ __forceinline__ uint32_t mx_dpp(uint32_t v) {
@@ -168,6 +226,10 @@ struct MxGemm {
     const float* row_scale;      // optional: factor of row r
 };
 hipError_t launch_mx_gemm(const MxGemm& g, hipStream_t st);
+// whether launch_mx_linear takes this product: x (c) cast on the way, no
+// operand a (g.a_q and g.a_sf unused)
+bool mx_linear_casts(int64_t M, int64_t N, int64_t Kp);
+hipError_t launch_mx_linear(const MxGemm& g, const MxCast& c, hipStream_t st);
 
 struct MxWgrad {
     const uint8_t *a_q, *a_sf;   // [N][Tp/2], a segment of 128-element steps per group

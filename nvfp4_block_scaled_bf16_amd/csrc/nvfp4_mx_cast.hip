@@ -17,62 +17,6 @@ namespace {
 // keeps the word of row i, so the 16 rows' words leave in one store.
 constexpr int kRowsPerWave = 16, kRowCols = 512;
 
-template <int T>
-struct Eight {                       // 8 elements of one row
-    uint32_t w[T == MX_F32 ? 8 : 4];
-};
-
-template <int T>
-__device__ __forceinline__ Eight<T> load_eight(const char* p, int valid) {
-    constexpr int B = T == MX_F32 ? 4 : 2;
-    Eight<T> v;
-    if (valid >= 8) {
-        __builtin_memcpy(&v, p, sizeof v);   // any alignment: the hardware splits what it has to
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8 * B / 4; ++i) {
-            if constexpr (T == MX_F32) {
-                v.w[i] = i < valid ? *(const uint32_t*)(p + 4 * i) : 0u;
-            } else {
-                const uint32_t lo = 2 * i < valid ? *(const uint16_t*)(p + 4 * i) : 0u;
-                const uint32_t hi = 2 * i + 1 < valid ? *(const uint16_t*)(p + 4 * i + 2) : 0u;
-                v.w[i] = lo | hi << 16;
-            }
-        }
-    }
-    return v;
-}
-
-template <int T>
-__device__ __forceinline__ uint32_t eight_mag(const Eight<T>& v) {
-    if constexpr (T == MX_F32) {
-        uint32_t m = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const uint32_t a = v.w[i] & 0x7fffffffu;
-            m = a > m ? a : m;
-        }
-        return m;
-    } else {
-        return max_halves(pk_max_u16(pk_max_u16(abs2(v.w[0]), abs2(v.w[1])), pk_max_u16(abs2(v.w[2]), abs2(v.w[3]))));
-    }
-}
-
-template <int T>
-__device__ __forceinline__ uint32_t eight_codes(const Eight<T>& v, float scale) {
-    if constexpr (T == MX_F32) {
-        uint32_t q = mx_put32<0>(0u, v.w[0], v.w[1], scale);
-        q = mx_put32<1>(q, v.w[2], v.w[3], scale);
-        q = mx_put32<2>(q, v.w[4], v.w[5], scale);
-        return mx_put32<3>(q, v.w[6], v.w[7], scale);
-    } else {
-        uint32_t q = mx_put16<T, 0>(0u, v.w[0], scale);
-        q = mx_put16<T, 1>(q, v.w[1], scale);
-        q = mx_put16<T, 2>(q, v.w[2], scale);
-        return mx_put16<T, 3>(q, v.w[3], scale);
-    }
-}
-
 template <int T, bool GATHER>
 __global__ __launch_bounds__(256) void k_mx_rows(MxCast c, uint32_t nchunk) {
     constexpr int B = T == MX_F32 ? 4 : 2;

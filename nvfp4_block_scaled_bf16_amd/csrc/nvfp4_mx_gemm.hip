@@ -125,14 +125,14 @@ __device__ __forceinline__ void store_slab(const T* slab, T* out, int64_t N, int
     }
 }
 
-template <int BM, int BN, int WM, int WN, int MODE>
+template <int BM, int BN, int WM, int WN, int ST, int MODE>
 __global__ __launch_bounds__(64 * WM * WN) void k_mx_gemm(TileArgs p) {
     constexpr int NT = 64 * WM * WN, FM = BM / WM / 32, FN = BN / WN / 32;
     // loads a thread issues per stage: of a's codes, b's and the scales
-    constexpr int QA = BM * 8 / NT, QB = BN * 8 / NT, SL = 2 * (BM + BN) / NT, L = QA + QB + SL;
-    static_assert(BM * 8 % NT == 0 && BN * 8 % NT == 0 && 2 * (BM + BN) % NT == 0 && BM % 64 == 0 && BN % 64 == 0, "");
-    static_assert(WM * WN * kSlab <= 2 * (int)sizeof(GemmStage<BM, BN>), "");
-    __shared__ __attribute__((aligned(16))) GemmStage<BM, BN> S[2];
+    constexpr int QA = BM * 8 / NT, QB = BN * 8 / NT, SL = (2 * (BM + BN) + NT - 1) / NT, L = QA + QB + SL;
+    static_assert(BM * 8 % NT == 0 && BN * 8 % NT == 0 && BM % 64 == 0 && BN % 64 == 0, "");
+    static_assert(WM * WN * kSlab <= ST * (int)sizeof(GemmStage<BM, BN>), "");
+    __shared__ __attribute__((aligned(16))) GemmStage<BM, BN> S[ST];
     const int tid = (int)threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave / WN, wn = wave % WN, half = lane >> 5, lr = lane & 31;
 
@@ -213,14 +213,16 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_gemm(TileArgs p) {
             qb[i] = (uint32_t)(n0 + r < p.N ? r : p.N - 1 - n0) * (uint32_t)(p.Kt * 64) + 16 * qc;
         }
         // scale words: the stage's first step's of all rows, then the second's
+        // (waves left over bring some again)
         const uint8_t* sp[SL];
-        int second[SL];
+        int second[SL], sdst[SL];
 #pragma unroll
         for (int i = 0; i < SL; ++i) {
-            const int first = 64 * wave + NT * i, w = first >= BM + BN, f = first - w * (BM + BN), r = f + lane;
+            const int first = (64 * wave + NT * i) % (2 * (BM + BN)), w = first >= BM + BN, f = first - w * (BM + BN), r = f + lane;
             const int64_t row = f < BM ? arow(r) : (n0 + r - BM < p.N ? n0 + r - BM : p.N - 1);
             sp[i] = (f < BM ? p.a_sf : b_sf) + mx_sf_offset(row, step0, p.Kt);
             second[i] = w ? 512 : 0;
+            sdst[i] = first;
         }
         const int64_t nst = (steps + 1) >> 1, nfull = steps >> 1;
         // an odd last step's stage takes it twice, the second time as zeros
@@ -234,7 +236,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_gemm(TileArgs p) {
                 load16_to_lds(bbase + k * 128 + (qb[n - QA] - bb), &st.q[128 * BM + 16 * (64 * wave + NT * (n - QA))]);
             } else {
                 const int i = n - QA - QB;
-                load4_to_lds(sp[i] + k * 1024 + (cut ? 0 : second[i]), &st.sf[0][64 * wave + NT * i]);
+                load4_to_lds(sp[i] + k * 1024 + (cut ? 0 : second[i]), &st.sf[0][sdst[i]]);
             }
         };
 
@@ -284,35 +286,39 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_gemm(TileArgs p) {
         using Q3 = std::integral_constant<int, 3>;
         Frags f0, f1;
         Scales sc, sn;
-        // A stage's loads begin in the last quarter of the stage two before it,
-        // whose place it takes, and end two quarters on
+        // A stage's loads begin in the last quarter of the stage ST before it,
+        // whose place it takes, and end a quarter on
         constexpr int L1 = L / 2;
+        auto clamped = [&](int64_t k) { return k < nst ? k : nst - 1; };
 #pragma unroll
-        for (int n = 0; n < L; ++n) bring(n, 0, S[0]);
+        for (int u = 0; u < ST; ++u)
 #pragma unroll
-        for (int n = 0; n < L1; ++n) bring(n, nst > 1 ? 1 : 0, S[1]);
-        asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(L1) : "memory");
+            for (int n = 0; n < (u + 1 < ST ? L : L1); ++n) bring(n, clamped(u), S[u]);
+        asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"((ST - 2) * L + L1) : "memory");
 #pragma unroll
         for (int z = 0; z < FM + FN; ++z) {
             read(S[0], 0, z, f0);
             read_scale(S[0], z, sc);
         }
-        auto stage = [&](int64_t s, GemmStage<BM, BN>& cur, GemmStage<BM, BN>& oth) __attribute__((always_inline)) {
+        // cur: the stage's place; last: that of the stage before it, whose
+        // successor's loads end here
+        auto stage = [&](int64_t s, GemmStage<BM, BN>& last, GemmStage<BM, BN>& cur, GemmStage<BM, BN>& next) __attribute__((always_inline)) {
             // past the last stage its loads come again, into a place that nobody reads
-            const int64_t k1 = s + 1 < nst ? s + 1 : nst - 1, k2 = s + 2 < nst ? s + 2 : nst - 1;
+            const int64_t k1 = clamped(s + ST - 1), k2 = clamped(s + ST);
             __builtin_amdgcn_sched_barrier(0);
-            quarter(Q0{}, f0, sc, f1, cur, 1, nullptr, L1, L, k1, oth);
-            quarter(Q1{}, f1, sc, f0, cur, 2, nullptr, L, L, k1, oth);
-            quarter(Q2{}, f0, sc, f1, cur, 3, nullptr, L, L, k1, oth);
+            quarter(Q0{}, f0, sc, f1, cur, 1, nullptr, L1, L, k1, last);
+            quarter(Q1{}, f1, sc, f0, cur, 2, nullptr, L, L, k1, last);
+            quarter(Q2{}, f0, sc, f1, cur, 3, nullptr, L, L, k1, last);
             // the next stage has landed, and this one has been read by every wave
-            asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+            asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((ST - 2) * L) : "memory");
             __builtin_amdgcn_sched_barrier(0);
-            quarter(Q3{}, f1, sc, f0, oth, 0, &sn, 0, L1, k2, cur);
+            quarter(Q3{}, f1, sc, f0, next, 0, &sn, 0, L1, k2, cur);
             sc = sn;
         };
-        for (int64_t s = 0; s < nfull; s += 2) {
-            stage(s, S[0], S[1]);
-            if (s + 1 < nfull) stage(s + 1, S[1], S[0]);
+        for (int64_t s = 0; s < nfull; s += ST) {
+#pragma unroll
+            for (int u = 0; u < ST; ++u)
+                if (s + u < nfull) stage(s + u, S[(u + ST - 1) % ST], S[u], S[(u + 1) % ST]);
         }
         if (nst > nfull) {
             auto drop = [&](Frags& f) __attribute__((always_inline)) {
@@ -321,7 +327,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_gemm(TileArgs p) {
             };
 #pragma unroll
             for (int z = 0; z < FM + FN; ++z) sc.v[z] = half ? 0 : sc.v[z];
-            GemmStage<BM, BN>& cur = S[nfull & 1];
+            GemmStage<BM, BN>& cur = S[nfull % ST];
             drop(f0);
             quarter(Q0{}, f0, sc, f1, cur, 1, nullptr, L, L, 0, cur);
             drop(f1);
@@ -389,7 +395,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_gemm(TileArgs p) {
     }
 }
 
-template <int BM, int BN, int WM, int WN, int MODE>
+template <int BM, int BN, int WM, int WN, int ST, int MODE>
 hipError_t launch_tiles(TileArgs p, int64_t mtiles, int64_t batch, hipStream_t st) {
     const int64_t ntn = (p.N + BN - 1) / BN;
     const int64_t grid = mtiles * ntn * batch;
@@ -397,30 +403,334 @@ hipError_t launch_tiles(TileArgs p, int64_t mtiles, int64_t batch, hipStream_t s
     if (grid == 0) return hipSuccess;
     p.ntm = (uint32_t)mtiles;
     p.ntn = (uint32_t)ntn;
-    k_mx_gemm<BM, BN, WM, WN, MODE><<<(unsigned)grid, 64 * WM * WN, 0, st>>>(p);
+    k_mx_gemm<BM, BN, WM, WN, ST, MODE><<<(unsigned)grid, 64 * WM * WN, 0, st>>>(p);
     return hipGetLastError();
 }
 
+// ------------------------------------------------------------- few rows
+//
+// Bound by the weights' bytes (17 bits per 32 elements).  A workgroup takes 16
+// NT vectors of b and up to 16 MT rows of a; its waves split the sum, each
+// streaming its part of b from memory straight into the registers of
+// v_mfma_scale 16x16x128 (lane l: vector l % 16, block l / 16 of the step),
+// kDeep steps ahead.  The waves' sums are added in LDS in their order.
+//
+// IN >= 0: a is x itself, of that type: the workgroup casts its rows into LDS
+// while its first loads of b are on their way, instead of a launch before it.
+
+constexpr int kDeep = 2;
+
+struct SkinnyArgs {
+    TileArgs t;
+    const void* x;
+    int64_t K, ldx;
+    int unit;                   // rows of a to a workgroup, at most 16 MT
+};
+
+template <int MT, int NT, int W, int IN, bool GROUPED>
+__global__ __launch_bounds__(64 * W) void k_mx_skinny(SkinnyArgs p) {
+    extern __shared__ __attribute__((aligned(16))) char lds[];
+    const int tid = (int)threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int lr = lane & 15, g = lane >> 4;
+    const TileArgs& t = p.t;
+    const uint32_t id = GROUPED ? xcd_index() : blockIdx.x;
+    const int64_t n0 = (int64_t)(id % t.ntn) * (16 * NT);
+    int64_t m0 = (int64_t)(id / t.ntn) * p.unit, mend = t.M;
+    const uint8_t *b_q = t.b_q, *b_sf = t.b_sf;
+    if constexpr (GROUPED) {
+        const MxGroupTile gt = mx_find_group(t.offsets, t.E, t.R, p.unit, id / t.ntn);
+        if (gt.e < 0) return;
+        m0 = gt.begin;
+        mend = gt.end;
+        b_q += (int64_t)gt.e * t.N * t.Kt * 64;
+        b_sf += (int64_t)gt.e * ((t.N + 127) / 128) * t.Kt * 512;
+    }
+    const int nrow = (int)(mend - m0 < p.unit ? mend - m0 : p.unit);
+    auto source = [&](int r) {                  // the vector of a of row r of the tile
+        int64_t row = m0 + (r < nrow ? r : nrow - 1);
+        if (GROUPED && t.rows) row = t.rows[row];
+        return row;
+    };
+
+    // this wave's steps: an even share of the pairs of steps, in one run
+    const int Kt = (int)t.Kt, pairs = (Kt + 1) / 2, first = pairs * wave / W * 2, last = pairs * (wave + 1) / W * 2;
+    const int cnt = (last < Kt ? last : Kt) - first;
+
+    // vectors past the last repeat it, their sums are not stored
+    const uint8_t *bq[NT], *bs[NT];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+        const int64_t n = n0 + 16 * j + lr < t.N ? n0 + 16 * j + lr : t.N - 1;
+        bq[j] = b_q + n * t.Kt * 64 + 16 * g;
+        bs[j] = b_sf + mx_sf_offset(n, 0, t.Kt);
+    }
+    const uint8_t *aq[MT], *as[MT];
+    bool none[MT];                              // a row index outside a: a row of zeros
+    if constexpr (IN < 0) {
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+            int64_t row = source(16 * i + lr);
+            none[i] = row < 0 || row >= t.A;
+            row = none[i] ? 0 : row;
+            aq[i] = t.a_q + row * t.Kt * 64 + 16 * g;
+            as[i] = t.a_sf + mx_sf_offset(row, 0, t.Kt);
+        }
+    }
+    struct Step {
+        u32x4 b[NT], a[IN < 0 ? MT : 1];
+        uint32_t bs[NT], as[IN < 0 ? MT : 1];
+    };
+    Step ring[kDeep];
+    auto load = [&](int i, Step& s) __attribute__((always_inline)) {
+        const int64_t k = first + (i < cnt ? i : cnt - 1);
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+            s.b[j] = *(const u32x4*)(bq[j] + k * 64);
+            s.bs[j] = *(const uint32_t*)(bs[j] + k * 512);
+        }
+        if constexpr (IN < 0) {
+#pragma unroll
+            for (int j = 0; j < MT; ++j) {
+                s.a[j] = *(const u32x4*)(aq[j] + k * 64);
+                s.as[j] = *(const uint32_t*)(as[j] + k * 512);
+            }
+        }
+    };
+    if (cnt > 0) {
+#pragma unroll
+        for (int d = 0; d < kDeep; ++d) load(d, ring[d]);
+    }
+
+    const int pitch = Kt * 64 + 16;             // of a row's codes in LDS
+    uint8_t* const lsf = (uint8_t*)lds + p.unit * pitch;
+    if constexpr (IN >= 0) {
+        constexpr int B = IN == MX_F32 ? 4 : 2;
+        const int per = Kt * 4;
+        for (int i = tid; i < nrow * per; i += 64 * W) {
+            const int r = i / per, blk = i - r * per;
+            const int64_t row = source(r), left = p.K - 32 * (int64_t)blk;
+            const bool have = row >= 0 && row < t.A;
+            Eight<IN> v[4];
+            uint32_t m = 0;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int64_t l = left - 8 * q;
+                v[q] = load_eight<IN>((const char*)p.x + (row * p.ldx + 32 * blk + 8 * q) * B,
+                                      have ? (l >= 8 ? 8 : (l > 0 ? (int)l : 0)) : 0);
+                const uint32_t e = eight_mag<IN>(v[q]);
+                m = e > m ? e : m;
+            }
+            const uint32_t code = mx_scale_code(mx_mag_bits<IN>(m));
+            const float sc = mx_cvt_scale(code);
+            *(u32x4*)(lds + r * pitch + 16 * blk) = u32x4{eight_codes<IN>(v[0], sc), eight_codes<IN>(v[1], sc),
+                                                           eight_codes<IN>(v[2], sc), eight_codes<IN>(v[3], sc)};
+            lsf[r * per + blk] = (uint8_t)code;
+        }
+        __syncthreads();
+    }
+
+    f32x4 acc[NT][MT];
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int i = 0; i < MT; ++i) acc[j][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    const int row = lr < nrow ? lr : nrow - 1;
+    auto use = [&](int i, const Step& s) __attribute__((always_inline)) {
+        u32x4 a[MT];
+        int sa[MT];
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+            if constexpr (IN >= 0) {
+                const int k = first + i;
+                a[m] = *(const u32x4*)(lds + row * pitch + k * 64 + 16 * g);
+                sa[m] = lsf[row * (Kt * 4) + 4 * k + g];
+            } else {
+                a[m] = none[m] ? u32x4{0, 0, 0, 0} : s.a[m];
+                sa[m] = none[m] ? 0 : (int)(s.as[m] >> (8 * g));
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+            const int sb = (int)(s.bs[j] >> (8 * g));
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+                acc[j][m] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(frag(s.b[j]), frag(a[m]), acc[j][m], kFp4,
+                                                                             kFp4, 0, sb, 0, sa[m]);
+        }
+    };
+    int i0 = 0;
+    for (; i0 + 2 * kDeep <= cnt; i0 += kDeep) {
+#pragma unroll
+        for (int d = 0; d < kDeep; ++d) {
+            use(i0 + d, ring[d]);
+            load(i0 + d + kDeep, ring[d]);
+        }
+    }
+#pragma unroll
+    for (int d = 0; d < kDeep; ++d) {
+        if (i0 + d < cnt) use(i0 + d, ring[d]);
+        if (i0 + d + kDeep < cnt) load(i0 + d + kDeep, ring[d]);
+    }
+#pragma unroll
+    for (int d = 0; d < kDeep; ++d)
+        if (i0 + d + kDeep < cnt) use(i0 + d + kDeep, ring[d]);
+
+    // the waves' sums: [wave][tile][lane], then 4 consecutive columns of one
+    // row to a thread
+    __syncthreads();
+    f32x4* const red = (f32x4*)lds;
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int i = 0; i < MT; ++i) red[(wave * NT * MT + j * MT + i) * 64 + lane] = acc[j][i];
+    __syncthreads();
+    for (int o = tid; o < NT * MT * 64; o += 64 * W) {
+        f32x4 v = red[o];
+#pragma unroll
+        for (int w = 1; w < W; ++w) v += red[w * NT * MT * 64 + o];
+        const int l = o & 63, tile = o >> 6, r = 16 * (tile % MT) + (l & 15);
+        const int64_t n = n0 + 16 * (tile / MT) + 4 * (l >> 4);
+        if (r >= nrow || n >= t.N) continue;
+        if (GROUPED && t.row_scale) {
+            const float f = t.row_scale[m0 + r];
+            // an outside row stays zero under an infinite factor
+            const int64_t src = source(r);
+            const bool zero = src < 0 || src >= t.A;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) v[c] = zero ? 0.0f : v[c] * f;
+        }
+        const int64_t at = (m0 + r) * t.N + n;
+        if (n + 4 <= t.N && t.N % 4 == 0 && ((uintptr_t)t.out & 15) == 0) {
+            if (t.type == MX_F32) *(f32x4*)((float*)t.out + at) = v;
+            else *(u32x2*)((uint16_t*)t.out + at) = u32x2{pack16(t.type, v[0], v[1]), pack16(t.type, v[2], v[3])};
+        } else {
+            for (int c = 0; c < 4 && n + c < t.N; ++c) {
+                if (t.type == MX_F32) ((float*)t.out)[at + c] = v[c];
+                else ((uint16_t*)t.out)[at + c] = (uint16_t)pack16(t.type, v[c], 0.0f);
+            }
+        }
+    }
+}
+
+
+template <int MT, int NT, int W, int IN, bool GROUPED>
+hipError_t launch_skinny(SkinnyArgs p, int64_t mtiles, hipStream_t st) {
+    const int64_t ntn = (p.t.N + 16 * NT - 1) / (16 * NT);
+    if (mtiles > kMxMaxGrid || ntn > kMxMaxGrid || mtiles * ntn > kMxMaxGrid) return hipErrorInvalidValue;
+    if (mtiles * ntn == 0) return hipSuccess;
+    p.t.ntn = (uint32_t)ntn;
+    const int red = W * NT * MT * 1024, codes = IN >= 0 ? p.unit * (int)(p.t.Kt * 68 + 16) : 0;
+    k_mx_skinny<MT, NT, W, IN, GROUPED><<<(unsigned)(mtiles * ntn), 64 * W, red > codes ? red : codes, st>>>(p);
+    return hipGetLastError();
+}
+// ---------------------------------------------------------------- choices
+
+// The tile shapes, by what a 128-element step of one tile costs in ns where it
+// is alone on its compute unit (`alone`) and, with as many as fit there
+// (`slots`), per tile (`full`): fits to products of 128 .. 16384 rows, 4096 and
+// 8192 columns and elements.
+struct TileCost { int bm, bn, slots, alone, full; };
+constexpr TileCost kTiles[] = {{256, 256, 1, 700, 700}, {256, 128, 1, 560, 560}, {128, 128, 2, 340, 305},
+                               {64, 128, 2, 228, 193}, {64, 64, 3, 205, 130}};
+constexpr int kNumTiles = 5;
+constexpr int64_t kCus = 256;
+
+// the shape whose `mtiles[i]` rows of tiles by N columns, `batch` times, take the least time
+int best_tile(const int64_t* mtiles, int64_t N, int64_t batch) {
+    int best = 0;
+    int64_t least = INT64_MAX;
+    for (int i = 0; i < kNumTiles; ++i) {
+        const TileCost& c = kTiles[i];
+        const int64_t each = (mtiles[i] * ((N + c.bn - 1) / c.bn) * batch + kCus - 1) / kCus;   // tiles of a compute unit
+        const int64_t rounds = (each + c.slots - 1) / c.slots, a = rounds * c.alone, f = each * c.full;
+        const int64_t cost = a > f ? a : f;
+        if (cost < least) {
+            least = cost;
+            best = i;
+        }
+    }
+    return best;
+}
+
+template <int MODE>
+hipError_t launch_best(const TileArgs& p, const int64_t* mtiles, int64_t batch, hipStream_t st) {
+    switch (best_tile(mtiles, p.N, batch)) {
+        case 0: return launch_tiles<256, 256, 4, 2, 2, MODE>(p, mtiles[0], batch, st);
+        case 1: return launch_tiles<256, 128, 4, 2, 2, MODE>(p, mtiles[1], batch, st);
+        case 2: return launch_tiles<128, 128, 2, 2, 2, MODE>(p, mtiles[2], batch, st);
+        case 3: return launch_tiles<64, 128, 2, 2, 3, MODE>(p, mtiles[3], batch, st);
+        default: return launch_tiles<64, 64, 2, 2, 3, MODE>(p, mtiles[4], batch, st);
+    }
+}
+
+template <int MT, int IN, bool GROUPED>
+hipError_t launch_few_nt(const SkinnyArgs& p, int64_t mtiles, hipStream_t st) {
+    // twice the columns to a workgroup where that leaves one for every compute unit
+    if (mtiles * ((p.t.N + 31) / 32) >= kCus) return launch_skinny<MT, 2, 4, IN, GROUPED>(p, mtiles, st);
+    return launch_skinny<MT, 1, 4, IN, GROUPED>(p, mtiles, st);
+}
+
+template <bool GROUPED>
+hipError_t launch_few(SkinnyArgs p, int64_t rows, int64_t mtiles, hipStream_t st) {
+    if (rows <= 16) return launch_few_nt<1, -1, GROUPED>(p, mtiles, st);
+    if (rows <= 32) return launch_few_nt<2, -1, GROUPED>(p, mtiles, st);
+    if (rows <= 48) return launch_few_nt<3, -1, GROUPED>(p, mtiles, st);
+    return launch_few_nt<4, -1, GROUPED>(p, mtiles, st);
+}
+
+// Rows of x that a workgroup can hold as codes (0: too long a row): up to 16,
+// in at most 36 KB, so that four workgroups fit a compute unit.
+int cast_rows(int64_t Kt) {
+    const int64_t n = 36 * 1024 / (Kt * 68 + 16);
+    return (int)(n < 16 ? n : 16);
+}
+
+// The few-rows kernel reads all of a for every 16 or 32 columns, from the L2:
+// past this many outputs that costs more than what the tiles lose (8192 x
+// 8192: 64 rows 15 us against 16, 128 rows 27 against 16).
+constexpr int64_t kFewOutputs = int64_t(1) << 19;
+
 }  // namespace
+
+bool mx_linear_casts(int64_t M, int64_t N, int64_t Kp) {
+    (void)N;
+    const int most = cast_rows(Kp / kMxStep);
+    return M <= (most < 8 ? most : 8);
+}
 
 hipError_t launch_mx_gemm(const MxGemm& g, hipStream_t st) {
     if (g.M <= 0 || g.N <= 0) return hipSuccess;
     TileArgs p{g.a_q, g.a_sf, g.b_q, g.b_sf, g.A, g.M, g.N, g.Kp / kMxStep, g.out, g.type, g.offsets, g.E, g.M,
                g.rows, g.row_scale, 0, 0};
+    int64_t mtiles[kNumTiles];
     if (g.offsets) {
-        if (g.M >= 256 * (int64_t)g.E) return launch_tiles<256, 256, 4, 2, GEMM_GROUPED>(p, mx_max_tiles(g.M, g.E, 256), 1, st);
-        return launch_tiles<128, 128, 2, 2, GEMM_GROUPED>(p, mx_max_tiles(g.M, g.E, 128), 1, st);
+        for (int i = 0; i < kNumTiles; ++i) mtiles[i] = mx_max_tiles(g.M, g.E, kTiles[i].bm);
+        return launch_best<GEMM_GROUPED>(p, mtiles, 1, st);
     }
-    if (((g.M + 255) / 256) * ((g.N + 255) / 256) >= 256)
-        return launch_tiles<256, 256, 4, 2, GEMM_DENSE>(p, (g.M + 255) / 256, 1, st);
-    return launch_tiles<128, 128, 2, 2, GEMM_DENSE>(p, (g.M + 127) / 128, 1, st);
+    if (g.M <= kFewOutputs / g.N) {
+        const SkinnyArgs s{p, nullptr, g.Kp, 0, g.M <= 64 ? (int)((g.M + 15) / 16 * 16) : 64};
+        return launch_few<false>(s, s.unit, (g.M + s.unit - 1) / s.unit, st);
+    }
+    for (int i = 0; i < kNumTiles; ++i) mtiles[i] = (g.M + kTiles[i].bm - 1) / kTiles[i].bm;
+    return launch_best<GEMM_DENSE>(p, mtiles, 1, st);
+}
+
+hipError_t launch_mx_linear(const MxGemm& g, const MxCast& c, hipStream_t st) {
+    TileArgs p{nullptr, nullptr, g.b_q, g.b_sf, g.A, g.M, g.N, g.Kp / kMxStep, g.out, g.type, g.offsets, g.E, g.M,
+               g.rows, g.row_scale, 0, 0};
+    const SkinnyArgs s{p, c.x, c.K, c.ldx, (int)g.M};
+    if (c.type == MX_F32) return launch_skinny<1, 1, 4, MX_F32, false>(s, 1, st);
+    if (c.type == MX_BF16) return launch_skinny<1, 1, 4, MX_BF16, false>(s, 1, st);
+    return launch_skinny<1, 1, 4, MX_F16, false>(s, 1, st);
 }
 
 hipError_t launch_mx_wgrad(const MxWgrad& g, hipStream_t st) {
     if (g.N <= 0 || g.K <= 0 || g.E <= 0) return hipSuccess;
     TileArgs p{g.a_q, g.a_sf, g.b_q, g.b_sf, g.N, g.N, g.K, g.Tp / kMxStep, g.out, g.type, g.offsets, g.E, g.Tp,
                nullptr, nullptr, 0, 0};
-    return launch_tiles<128, 128, 2, 2, GEMM_WGRAD>(p, (g.N + 127) / 128, g.E, st);
+    int64_t mtiles[kNumTiles];
+    for (int i = 0; i < kNumTiles; ++i) mtiles[i] = (g.N + kTiles[i].bm - 1) / kTiles[i].bm;
+    return launch_best<GEMM_WGRAD>(p, mtiles, g.E, st);
 }
 
 }  // namespace nvfp4
