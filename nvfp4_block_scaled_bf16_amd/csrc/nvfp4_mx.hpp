@@ -138,6 +138,11 @@ template <int CTRL>
 __device__ __forceinline__ uint32_t mx_dpp(uint32_t v) {
     return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xf, 0xf, false);
 }
+// the exchange's value, 0 where the pattern has no source lane or leaves the row out
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int mx_dpp_or_0(int v) {
+    return __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xf, true);
+}
 constexpr int kDppXor1 = 0xB1, kDppXor2 = 0x4E;   // quad_perm [1,0,3,2] and [2,3,0,1]
 constexpr int kDppRor4 = 0x124, kDppRor8 = 0x128, kDppRor2 = 0x122, kDppRor1 = 0x121;
 
@@ -172,21 +177,24 @@ __device__ __forceinline__ MxGroupTile mx_find_group(const int32_t* __restrict__
     for (int e0 = 0; e0 < E; e0 += 64) {
         int64_t a = 0, b = 0;
         if (e0 + lane < E) mx_group_rows(offsets, e0 + lane, R, &a, &b);
-        int n = (int)((b - a + unit - 1) / unit);
+        const int n = (int)(b - a + unit - 1) / unit;
+        // inclusive scan: within rows of 16 lanes, then over the rows
         int s = n;
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const int v = __shfl_up(s, d, 64);
-            if (lane >= d) s += v;
-        }
+        s += mx_dpp_or_0<0x111, 0xf>(s);    // row_shr 1, 2, 4, 8
+        s += mx_dpp_or_0<0x112, 0xf>(s);
+        s += mx_dpp_or_0<0x114, 0xf>(s);
+        s += mx_dpp_or_0<0x118, 0xf>(s);
+        s += mx_dpp_or_0<0x142, 0xa>(s);    // lane 15 of rows 0 and 2 to rows 1 and 3
+        s += mx_dpp_or_0<0x143, 0xc>(s);    // lane 31 to rows 2 and 3
         const uint64_t past = __ballot(base + s > t);
         if (past) {
             const int l = __builtin_ctzll(past);
-            const int64_t ga = __shfl((long long)a, l, 64), gb = __shfl((long long)b, l, 64);
-            const int64_t first = base + __shfl(s - n, l, 64);
+            // rows are 31-bit, held to R
+            const int64_t ga = __builtin_amdgcn_readlane((int)a, l), gb = __builtin_amdgcn_readlane((int)b, l);
+            const int64_t first = base + __builtin_amdgcn_readlane(s - n, l);
             return MxGroupTile{e0 + l, ga + (t - first) * unit, gb};
         }
-        base += __shfl(s, 63, 64);
+        base += __builtin_amdgcn_readlane(s, 63);
     }
     return MxGroupTile{-1, 0, 0};
 }

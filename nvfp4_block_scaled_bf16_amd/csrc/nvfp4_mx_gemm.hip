@@ -56,7 +56,10 @@ __device__ __forceinline__ uint32_t pack16(int type, float a, float b) {
 // LDS read and load placed between MFMAs 575 (the reads alone held up the
 // MFMAs for 400 cycles a step, the loads, half a line each, for another 400).
 
-enum GemmMode { GEMM_DENSE, GEMM_GROUPED, GEMM_WGRAD };
+// GEMM_GROUPED_FAR: an operand a of 4 GB or more, whose rows need 64-bit offsets
+// (two more vector additions a load: 32768 rows of 4096 over 64 experts took 8 %
+// longer)
+enum GemmMode { GEMM_DENSE, GEMM_GROUPED, GEMM_GROUPED_FAR, GEMM_WGRAD };
 
 template <int BM, int BN>
 struct GemmStage {
@@ -128,6 +131,7 @@ __device__ __forceinline__ void store_slab(const T* slab, T* out, int64_t N, int
 template <int BM, int BN, int WM, int WN, int ST, int MODE>
 __global__ __launch_bounds__(64 * WM * WN) void k_mx_gemm(TileArgs p) {
     constexpr int NT = 64 * WM * WN, FM = BM / WM / 32, FN = BN / WN / 32;
+    constexpr bool GROUPED = MODE == GEMM_GROUPED || MODE == GEMM_GROUPED_FAR;
     // loads a thread issues per stage: of a's codes, b's and the scales
     constexpr int QA = BM * 8 / NT, QB = BN * 8 / NT, SL = (2 * (BM + BN) + NT - 1) / NT, L = QA + QB + SL;
     static_assert(BM * 8 % NT == 0 && BN * 8 % NT == 0 && BM % 64 == 0 && BN % 64 == 0, "");
@@ -162,7 +166,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_gemm(TileArgs p) {
             if (step0 + steps > p.Kt) steps = p.Kt > step0 ? p.Kt - step0 : 0;
             out0 = (int64_t)e * p.M * p.N;
         }
-        if constexpr (MODE == GEMM_GROUPED) {
+        if constexpr (GROUPED) {
             tn = id % p.ntn;
             const MxGroupTile g = mx_find_group(p.offsets, p.E, p.R, BM, id / p.ntn);
             if (g.e < 0) return;
@@ -188,9 +192,9 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_gemm(TileArgs p) {
     if (steps > 0) {
         // Sources of this thread's loads: row (tid + NT i) / 8 of the tile,
         // chunk qc.  Rows past the end repeat the last one, whose products are
-        // not stored.  Grouped rows can be anywhere in a: 64-bit offsets.
-        constexpr bool GA = MODE == GEMM_GROUPED;
-        typedef typename std::conditional<GA, int64_t, uint32_t>::type AOff;
+        // not stored.  Grouped rows can be anywhere in a.
+        constexpr bool GA = GROUPED;
+        typedef typename std::conditional<MODE == GEMM_GROUPED_FAR, int64_t, uint32_t>::type AOff;
         const uint8_t* const abase = GA ? p.a_q : p.a_q + (m0 * p.Kt + step0) * 64;
         const uint8_t* const bbase = b_q + (n0 * p.Kt + step0) * 64;
         auto arow = [&](int r) {
@@ -355,7 +359,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_gemm(TileArgs p) {
         const int nrow = (int)(mend - row0 < 32 ? mend - row0 : 32);
         float f = 1.0f;
         bool zero = false;
-        if constexpr (MODE == GEMM_GROUPED) {
+        if constexpr (GROUPED) {
             if (row < mend) {
                 if (p.row_scale) f = p.row_scale[row];
                 // a row index outside a stands for a row of zeros
@@ -705,6 +709,7 @@ hipError_t launch_mx_gemm(const MxGemm& g, hipStream_t st) {
     int64_t mtiles[kNumTiles];
     if (g.offsets) {
         for (int i = 0; i < kNumTiles; ++i) mtiles[i] = mx_max_tiles(g.M, g.E, kTiles[i].bm);
+        if (g.A >= (int64_t(1) << 32) / (g.Kp / 2)) return launch_best<GEMM_GROUPED_FAR>(p, mtiles, 1, st);
         return launch_best<GEMM_GROUPED>(p, mtiles, 1, st);
     }
     if (g.M <= kFewOutputs / g.N) {
