@@ -10,49 +10,60 @@ namespace {
 
 // ------------------------------------------------------------- rowwise only
 //
-// A wave takes 16 rows by 512 columns: 8 elements a lane, one 1-KiB (2-byte
+// A wave takes RPW rows by 512 columns: 8 elements a lane, one 1-KiB (2-byte
 // types) run of a row per load.  Four lanes share a block: its maximum takes
 // two lane exchanges, and a lane's 8 codes are one word of the output.  A
 // 16-lane group holds the four scales of one 128-element step; lane i of it
-// keeps the word of row i, so the 16 rows' words leave in one store.
-constexpr int kRowsPerWave = 16, kRowCols = 512;
+// keeps the word of row i, so the rows' words leave in one store.  16 rows a
+// wave fill the scale words' cache lines; few rows are spread over more waves,
+// one to a wave in the end (1 x 4096: 7.8 us with 16, the other 15 empty).
+constexpr int kRowCols = 512;
 
-template <int T, bool GATHER>
+template <int T, bool GATHER, int RPW>
 __global__ __launch_bounds__(256) void k_mx_rows(MxCast c, uint32_t nchunk) {
-    constexpr int B = T == MX_F32 ? 4 : 2;
+    constexpr int B = T == MX_F32 ? 4 : 2, AHEAD = RPW < 4 ? RPW : 4;
     const int lane = (int)(threadIdx.x & 63), wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-    const int64_t r0 = ((int64_t)(blockIdx.x / nchunk) * 4 + wave) * kRowsPerWave;
+    const int64_t r0 = ((int64_t)(blockIdx.x / nchunk) * 4 + wave) * RPW;
     const int64_t c0 = (int64_t)(blockIdx.x % nchunk) * kRowCols + 8 * lane;
     const int64_t Kt = (c.K + kMxStep - 1) / kMxStep;
     const int64_t left = c.K - c0;
     const int valid = left >= 8 ? 8 : (left > 0 ? (int)left : 0);
     const int64_t kb = c0 / kMxStep;
     int idx = 0;
-    if constexpr (GATHER) idx = r0 + (lane & 15) < c.R ? c.rows[r0 + (lane & 15)] : -1;
+    if constexpr (GATHER) idx = (lane & 15) < RPW && r0 + (lane & 15) < c.R ? c.rows[r0 + (lane & 15)] : -1;
     uint32_t keep = 0;
-#pragma unroll 4
-    for (int i = 0; i < kRowsPerWave; ++i) {
-        const int64_t r = r0 + i;
-        int64_t src = r;
-        if constexpr (GATHER) src = __builtin_amdgcn_readlane(idx, i);
-        const bool have = r < c.R && src >= 0 && src < c.M;
-        const Eight<T> v = load_eight<T>((const char*)c.x + (src * c.ldx + c0) * B, have ? valid : 0);
-        uint32_t m = eight_mag<T>(v), o;
-        o = mx_dpp<kDppXor1>(m);
-        m = o > m ? o : m;
-        o = mx_dpp<kDppXor2>(m);
-        m = o > m ? o : m;
-        const uint32_t code = mx_scale_code(mx_mag_bits<T>(m));
-        const uint32_t q = eight_codes<T>(v, mx_cvt_scale(code));
-        if (r < c.R && kb < Kt) *(uint32_t*)(c.row_q + r * (Kt * (kMxStep / 2)) + c0 / 2) = q;
-        uint32_t word = code << (8 * ((lane >> 2) & 3));
-        word |= mx_dpp<kDppRor4>(word);
-        word |= mx_dpp<kDppRor8>(word);
-        keep = (lane & 15) == i ? word : keep;
+#pragma unroll
+    for (int i0 = 0; i0 < RPW; i0 += AHEAD) {
+        if (r0 + i0 >= c.R) break;
+        Eight<T> v[AHEAD];
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            const int64_t r = r0 + i0 + i;
+            int64_t src = r;
+            if constexpr (GATHER) src = __builtin_amdgcn_readlane(idx, i0 + i);
+            const bool have = r < c.R && src >= 0 && src < c.M;
+            v[i] = load_eight<T>((const char*)c.x + (src * c.ldx + c0) * B, have ? valid : 0);
+        }
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            const int64_t r = r0 + i0 + i;
+            uint32_t m = eight_mag<T>(v[i]), o;
+            o = mx_dpp<kDppXor1>(m);
+            m = o > m ? o : m;
+            o = mx_dpp<kDppXor2>(m);
+            m = o > m ? o : m;
+            const uint32_t code = mx_scale_code(mx_mag_bits<T>(m));
+            const uint32_t q = eight_codes<T>(v[i], mx_cvt_scale(code));
+            if (r < c.R && kb < Kt) *(uint32_t*)(c.row_q + r * (Kt * (kMxStep / 2)) + c0 / 2) = q;
+            uint32_t word = code << (8 * ((lane >> 2) & 3));
+            word |= mx_dpp<kDppRor4>(word);
+            word |= mx_dpp<kDppRor8>(word);
+            keep = (lane & 15) == i0 + i ? word : keep;
+        }
     }
     // rows past R, up to the 128-row tile's end: scale code 0
     const int64_t r = r0 + (lane & 15);
-    if (kb < Kt && r < (c.R + 127) / 128 * 128) *(uint32_t*)(c.row_sf + mx_sf_offset(r, kb, Kt)) = keep;
+    if (kb < Kt && (lane & 15) < RPW && r < (c.R + 127) / 128 * 128) *(uint32_t*)(c.row_sf + mx_sf_offset(r, kb, Kt)) = keep;
 }
 
 // --------------------------------------------------------- both directions
@@ -310,16 +321,24 @@ __global__ __launch_bounds__(256) void k_mx_dequant(const uint8_t* __restrict__ 
     }
 }
 
+template <int T, int RPW>
+hipError_t launch_rows(const MxCast& c, int64_t chunks, hipStream_t st) {
+    const int64_t grid = chunks * ((c.R + 127) / 128 * (128 / (4 * RPW)));
+    if (grid > kMxMaxGrid) return hipErrorInvalidValue;
+    if (c.rows) k_mx_rows<T, true, RPW><<<(unsigned)grid, 256, 0, st>>>(c, (uint32_t)chunks);
+    else k_mx_rows<T, false, RPW><<<(unsigned)grid, 256, 0, st>>>(c, (uint32_t)chunks);
+    return hipGetLastError();
+}
+
 template <int T>
 hipError_t launch_cast(const MxCast& c, hipStream_t st) {
     const int64_t Kt = (c.K + kMxStep - 1) / kMxStep;
     if (!c.col_q) {
-        const int64_t chunks = (c.K + kRowCols - 1) / kRowCols, groups = (c.R + 127) / 128 * (128 / (4 * kRowsPerWave));
-        if (chunks * groups > kMxMaxGrid) return hipErrorInvalidValue;
-        const dim3 grid((unsigned)(chunks * groups));
-        if (c.rows) k_mx_rows<T, true><<<grid, 256, 0, st>>>(c, (uint32_t)chunks);
-        else k_mx_rows<T, false><<<grid, 256, 0, st>>>(c, (uint32_t)chunks);
-        return hipGetLastError();
+        const int64_t chunks = (c.K + kRowCols - 1) / kRowCols, runs = c.R * chunks;
+        // waves of 16, 4 or 1 rows: as many rows as leave 8 waves to a compute unit
+        if (runs >= 16 * 2048) return launch_rows<T, 16>(c, chunks, st);
+        if (runs >= 4 * 2048) return launch_rows<T, 4>(c, chunks, st);
+        return launch_rows<T, 1>(c, chunks, st);
     }
     const int64_t Tt = c.offsets ? mx_max_tiles(c.R, c.E, 128) : (c.R + 127) / 128;
     if (Tt * Kt > kMxMaxGrid) return hipErrorInvalidValue;

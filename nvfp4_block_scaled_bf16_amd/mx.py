@@ -16,13 +16,21 @@ One linear layer, forward and backward::
 """
 from __future__ import annotations
 
-import ctypes
-
 import torch
 
-from . import _check, _ptr, _stream, _u8, lib
+from . import _check, lib
 
 _TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+_U8 = torch.uint8
+
+# A decoding step calls these with microseconds of GPU work each, so the checks
+# below compare plain integers, pointers go to the library as such, and the
+# stream's handle comes without a Stream object around it (8 us less a call).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream(index):
+    return _raw_stream(index) if _raw_stream else torch.cuda.current_stream(index).cuda_stream
 
 
 def _up(n, m):
@@ -31,7 +39,7 @@ def _up(n, m):
 
 def mx_sf_shape(R: int, K: int) -> tuple:
     """Shape of the scale codes of R vectors of K elements."""
-    return (_up(R, 128) // 128, _up(K, 128) // 128, 128, 4)
+    return (-(-R // 128), -(-K // 128), 128, 4)
 
 
 def mx_padded_rows(R: int, num_groups: int) -> int:
@@ -41,49 +49,74 @@ def mx_padded_rows(R: int, num_groups: int) -> int:
 
 
 def _type(dtype, name):
-    try:
-        return _TYPES[dtype]
-    except KeyError:
-        raise ValueError(f"{name} must be float32, bfloat16 or float16 (got {dtype})") from None
-
-
-def _matrix(x, name="x"):
-    """A 2-D tensor with adjacent columns: its row pitch in elements."""
-    if not isinstance(x, torch.Tensor) or x.dim() != 2 or not x.is_cuda:
-        raise ValueError(f"{name} must be a 2-D CUDA tensor")
-    _type(x.dtype, name)
-    if x.shape[1] > 1 and x.stride(1) != 1:
-        raise ValueError(f"{name} must have adjacent columns (stride 1 in its last dimension)")
-    return x.stride(0) if x.shape[0] > 1 else x.shape[1]
-
-
-def _tensor(t, dtype, device, name, shape=None):
-    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor on {device}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have the shape {tuple(shape)} (got {tuple(t.shape)})")
+    t = _TYPES.get(dtype)
+    if t is None:
+        raise ValueError(f"{name} must be float32, bfloat16 or float16 (got {dtype})")
     return t
 
 
+def _matrix(x, name="x"):
+    """A 2-D tensor with adjacent columns: type, rows, columns and row pitch in
+    elements."""
+    if not isinstance(x, torch.Tensor) or x.dim() != 2 or not x.is_cuda:
+        raise ValueError(f"{name} must be a 2-D CUDA tensor")
+    M, K = x.shape
+    ld, step = x.stride()
+    if K > 1 and step != 1:
+        raise ValueError(f"{name} must have adjacent columns (stride 1 in its last dimension)")
+    return _type(x.dtype, name), M, K, ld if M > 1 else K
+
+
+def _tensor(t, dtype, index, name, shape=None):
+    """A contiguous tensor of this type on device `index`: its address."""
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or not t.is_contiguous() or t.get_device() != index or index < 0:
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor on the operands' GPU")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must have the shape {tuple(shape)} (got {tuple(t.shape)})")
+    return t.data_ptr()
+
+
 def _codes(q, sf, name, batch=False):
-    """Vectors and padded length of one operand (``batch``: one per group)."""
-    dims = 3 if batch else 2
-    if not isinstance(q, torch.Tensor) or q.dim() != dims or not q.is_cuda or q.shape[-1] % 64:
-        raise ValueError(f"{name}_q must be a {dims}-D uint8 CUDA tensor with rows of a multiple of 64 bytes")
-    _tensor(q, torch.uint8, q.device, f"{name}_q")
-    rows, Kp = q.shape[-2], 2 * q.shape[-1]
-    _tensor(sf, torch.uint8, q.device, f"{name}_sf", (q.shape[0],) * batch + mx_sf_shape(rows, Kp))
-    return rows, Kp
+    """One operand (``batch``: one per group): addresses, vectors, padded
+    length and device."""
+    if not isinstance(q, torch.Tensor) or q.dim() != 2 + batch or q.shape[-1] % 64:
+        raise ValueError(f"{name}_q must be a {2 + batch}-D uint8 CUDA tensor with rows of a multiple of 64 bytes")
+    index = q.get_device()
+    qp = _tensor(q, _U8, index, f"{name}_q")
+    shape = q.shape
+    rows, Kp = shape[-2], 2 * shape[-1]
+    want = mx_sf_shape(rows, Kp)
+    return qp, _tensor(sf, _U8, index, f"{name}_sf", (shape[0],) + want if batch else want), rows, Kp, index
 
 
-def _groups(offsets, rows, R, device):
-    if not isinstance(offsets, torch.Tensor) or offsets.dim() != 1 or offsets.numel() < 1:
+def _groups(offsets, rows, R, index):
+    """Addresses of offsets and rows, groups, and rows in all."""
+    if not isinstance(offsets, torch.Tensor) or offsets.dim() != 1 or offsets.shape[0] < 1:
         raise ValueError("offsets must be a 1-D int32 tensor of num_groups + 1 values")
-    _tensor(offsets, torch.int32, device, "offsets")
-    if rows is not None:
-        _tensor(rows, torch.int32, device, "rows", (rows.numel(),))
-        R = rows.numel()
-    return offsets.numel() - 1, R
+    op = _tensor(offsets, torch.int32, index, "offsets")
+    E = offsets.shape[0] - 1
+    if rows is None:
+        return op, None, E, R
+    if not isinstance(rows, torch.Tensor) or rows.dim() != 1:
+        raise ValueError("rows must be a 1-D int32 tensor")
+    return op, _tensor(rows, torch.int32, index, "rows"), E, rows.shape[0]
+
+
+def _outputs(x, rowwise, columnwise, R, K, Tp):
+    """Output tensors of a cast of R vectors of K (columnwise K of Tp), and
+    their addresses."""
+    out, p = {}, [None, None, None, None]
+    if rowwise:
+        q = out["row_q"] = x.new_empty((R, _up(K, 128) // 2), dtype=_U8)
+        sf = out["row_sf"] = x.new_empty(mx_sf_shape(R, K), dtype=_U8)
+        p[0], p[1] = q.data_ptr(), sf.data_ptr()
+    if columnwise:
+        q = out["col_q"] = x.new_empty((K, _up(Tp, 128) // 2), dtype=_U8)
+        sf = out["col_sf"] = x.new_empty(mx_sf_shape(K, Tp), dtype=_U8)
+        p[2], p[3] = q.data_ptr(), sf.data_ptr()
+    if not out:
+        raise ValueError("no output direction requested")
+    return out, p
 
 
 def mx_quantize(x: torch.Tensor, rowwise: bool = True, columnwise: bool = True) -> dict:
@@ -94,19 +127,12 @@ def mx_quantize(x: torch.Tensor, rowwise: bool = True, columnwise: bool = True) 
         t = mx_quantize(x.t(), columnwise, rowwise)
         swap = {"row": "col", "col": "row"}
         return {swap[k[:3]] + k[3:]: v for k, v in t.items()}
-    ldx = _matrix(x)
-    M, K = x.shape
-    dev, out = x.device, {}
-    if rowwise:
-        out.update(row_q=_u8((M, _up(K, 128) // 2), dev), row_sf=_u8(mx_sf_shape(M, K), dev))
-    if columnwise:
-        out.update(col_q=_u8((K, _up(M, 128) // 2), dev), col_sf=_u8(mx_sf_shape(K, M), dev))
-    g = out.get
-    if not out:
-        raise ValueError("no output direction requested")
+    t, M, K, ldx = _matrix(x)
+    out, p = _outputs(x, rowwise, columnwise, M, K, M)
     if M and K:
-        _check(lib().nvfp4_mx_quantize(_ptr(x), _TYPES[x.dtype], M, K, ldx, _ptr(g("row_q")), _ptr(g("row_sf")),
-                                       _ptr(g("col_q")), _ptr(g("col_sf")), _stream(dev)))
+        st = lib().nvfp4_mx_quantize(x.data_ptr(), t, M, K, ldx, *p, _stream(x.get_device()))
+        if st:
+            _check(st)
     return out
 
 
@@ -116,47 +142,49 @@ def mx_quantize_grouped(x: torch.Tensor, offsets: torch.Tensor, rows: torch.Tens
     hold: group e those from offsets[e] to offsets[e + 1], int32 on the device.
     Columnwise vectors have :func:`mx_padded_rows` elements, each group
     beginning a step of 128 of its own, for :func:`mx_wgrad_grouped`."""
-    ldx = _matrix(x)
-    M, K = x.shape
-    dev, out = x.device, {}
-    E, R = _groups(offsets, rows, M, dev)
-    if rowwise:
-        out.update(row_q=_u8((R, _up(K, 128) // 2), dev), row_sf=_u8(mx_sf_shape(R, K), dev))
-    if columnwise:
-        Tp = mx_padded_rows(R, E)
-        out.update(col_q=_u8((K, Tp // 2), dev), col_sf=_u8(mx_sf_shape(K, Tp), dev))
-    g = out.get
-    if not out:
-        raise ValueError("no output direction requested")
+    t, M, K, ldx = _matrix(x)
+    index = x.get_device()
+    op, rp, E, R = _groups(offsets, rows, M, index)
+    out, p = _outputs(x, rowwise, columnwise, R, K, mx_padded_rows(R, E))
     if R and K and (rowwise or E):
-        _check(lib().nvfp4_mx_quantize_grouped(_ptr(x), _TYPES[x.dtype], M, K, ldx, _ptr(rows), R, _ptr(offsets), E,
-                                               _ptr(g("row_q")), _ptr(g("row_sf")), _ptr(g("col_q")),
-                                               _ptr(g("col_sf")), _stream(dev)))
+        st = lib().nvfp4_mx_quantize_grouped(x.data_ptr(), t, M, K, ldx, rp, R, op, E, *p, _stream(index))
+        if st:
+            _check(st)
     return out
 
 
 def mx_dequantize(q: torch.Tensor, sf: torch.Tensor, K: int, out_dtype=torch.float32) -> torch.Tensor:
     """The values [R, K] that codes and scales stand for."""
-    R, Kp = _codes(q, sf, "mx")
+    qp, sp, R, Kp, index = _codes(q, sf, "mx")
     t = _type(out_dtype, "out_dtype")
     if not 0 <= K <= Kp or Kp != _up(K, 128):
         raise ValueError(f"K={K} does not fit rows of {Kp} codes")
-    out = torch.empty((R, K), dtype=out_dtype, device=q.device)
-    _check(lib().nvfp4_mx_dequantize(_ptr(q), _ptr(sf), R, K, t, _ptr(out), _stream(q.device)))
+    out = q.new_empty((R, K), dtype=out_dtype)
+    st = lib().nvfp4_mx_dequantize(qp, sp, R, K, t, out.data_ptr(), _stream(index))
+    if st:
+        _check(st)
     return out
 
 
 def mx_gemm(a_q, a_sf, b_q, b_sf, out_dtype=torch.bfloat16) -> torch.Tensor:
     """out [M, N] = a b^T for M vectors a and N vectors b, summed in fp32."""
-    M, K = _codes(a_q, a_sf, "a")
-    N, Kb = _codes(b_q, b_sf, "b")
-    if K != Kb or a_q.device != b_q.device:
+    ap, asp, M, K, index = _codes(a_q, a_sf, "a")
+    bp, bsp, N, Kb, bi = _codes(b_q, b_sf, "b")
+    if K != Kb or index != bi:
         raise ValueError("a and b differ in length or device")
     t = _type(out_dtype, "out_dtype")
-    out = torch.empty((M, N), dtype=out_dtype, device=a_q.device)
-    _check(lib().nvfp4_mx_gemm(_ptr(a_q), _ptr(a_sf), _ptr(b_q), _ptr(b_sf), M, N, K, t, _ptr(out),
-                               _stream(a_q.device)))
+    out = a_q.new_empty((M, N), dtype=out_dtype)
+    st = lib().nvfp4_mx_gemm(ap, asp, bp, bsp, M, N, K, t, out.data_ptr(), _stream(index))
+    if st:
+        _check(st)
     return out
+
+
+def _grouped_shapes(offsets, rows, row_scale, A, E_b, index, name):
+    op, rp, E, R = _groups(offsets, rows, A, index)
+    if E != E_b:
+        raise ValueError(f"offsets are for {E} groups, {name} for {E_b}")
+    return op, rp, E, R, None if row_scale is None else _tensor(row_scale, torch.float32, index, "row_scale", (R,))
 
 
 def mx_gemm_grouped(a_q, a_sf, b_q, b_sf, offsets, rows=None, row_scale=None,
@@ -164,20 +192,16 @@ def mx_gemm_grouped(a_q, a_sf, b_q, b_sf, offsets, rows=None, row_scale=None,
     """out [R, N]: for the rows r of group e, row_scale[r] * a[rows[r]] b_e^T.
     b_q [E, N, Kp/2] and b_sf hold one operand per group; rows of out that no
     group holds are not written."""
-    A, K = _codes(a_q, a_sf, "a")
-    N, Kb = _codes(b_q, b_sf, "b", batch=True)
-    dev = a_q.device
-    if K != Kb or b_q.device != dev:
+    ap, asp, A, K, index = _codes(a_q, a_sf, "a")
+    bp, bsp, N, Kb, bi = _codes(b_q, b_sf, "b", batch=True)
+    if K != Kb or index != bi:
         raise ValueError("a and b differ in length or device")
-    E, R = _groups(offsets, rows, A, dev)
-    if E != b_q.shape[0]:
-        raise ValueError(f"offsets are for {E} groups, b for {b_q.shape[0]}")
-    if row_scale is not None:
-        _tensor(row_scale, torch.float32, dev, "row_scale", (R,))
+    op, rp, E, R, fp = _grouped_shapes(offsets, rows, row_scale, A, b_q.shape[0], index, "b")
     t = _type(out_dtype, "out_dtype")
-    out = torch.empty((R, N), dtype=out_dtype, device=dev)
-    _check(lib().nvfp4_mx_gemm_grouped(_ptr(a_q), _ptr(a_sf), A, _ptr(rows), R, _ptr(offsets), E, _ptr(b_q),
-                                       _ptr(b_sf), N, K, _ptr(row_scale), t, _ptr(out), _stream(dev)))
+    out = a_q.new_empty((R, N), dtype=out_dtype)
+    st = lib().nvfp4_mx_gemm_grouped(ap, asp, A, rp, R, op, E, bp, bsp, N, K, fp, t, out.data_ptr(), _stream(index))
+    if st:
+        _check(st)
     return out
 
 
@@ -185,40 +209,45 @@ def mx_wgrad_grouped(a_q, a_sf, b_q, b_sf, offsets, out_dtype=torch.float32) -> 
     """out [E, N, K]: for each group the sum over its rows of a[n][r] b[k][r],
     from the columnwise outputs of :func:`mx_quantize_grouped` with the same
     offsets.  An empty group gives zeros."""
-    N, Tp = _codes(a_q, a_sf, "a")
-    K, Tb = _codes(b_q, b_sf, "b")
-    dev = a_q.device
-    if Tp != Tb or b_q.device != dev:
+    ap, asp, N, Tp, index = _codes(a_q, a_sf, "a")
+    bp, bsp, K, Tb, bi = _codes(b_q, b_sf, "b")
+    if Tp != Tb or index != bi:
         raise ValueError("a and b differ in length or device")
-    E, _ = _groups(offsets, None, 0, dev)
+    op, _, E, _ = _groups(offsets, None, 0, index)
     t = _type(out_dtype, "out_dtype")
-    out = torch.empty((E, N, K), dtype=out_dtype, device=dev)
-    _check(lib().nvfp4_mx_wgrad_grouped(_ptr(a_q), _ptr(a_sf), _ptr(b_q), _ptr(b_sf), N, K, Tp, _ptr(offsets), E, t,
-                                        _ptr(out), _stream(dev)))
+    out = a_q.new_empty((E, N, K), dtype=out_dtype)
+    st = lib().nvfp4_mx_wgrad_grouped(ap, asp, bp, bsp, N, K, Tp, op, E, t, out.data_ptr(), _stream(index))
+    if st:
+        _check(st)
     return out
 
 
-def _workspace(n, dev):
-    return _u8(n, dev) if n else None
+def _weights(x, w_q, w_sf, out_dtype, batch):
+    xt, M, K, ldx = _matrix(x)
+    wp, wsp, N, Kp, index = _codes(w_q, w_sf, "w", batch)
+    if Kp != _up(K, 128) or index != x.get_device():
+        raise ValueError(f"x of {K} columns does not fit weights of {Kp} codes on {w_q.device}")
+    out_dtype = out_dtype or x.dtype
+    return xt, M, K, ldx, wp, wsp, N, index, out_dtype, _type(out_dtype, "out_dtype")
+
+
+def _workspace(x, n):
+    # freed to the stream's order as soon as the call has been enqueued
+    return x.new_empty(n, dtype=_U8) if n else None
 
 
 def mx_linear(x: torch.Tensor, w_q, w_sf, out_dtype=None) -> torch.Tensor:
     """y [M, N] = Q(x) W^T for x [M, K] (cast on the way) and N weight vectors;
     of x's type unless ``out_dtype`` is given."""
-    ldx = _matrix(x)
-    M, K = x.shape
-    N, Kp = _codes(w_q, w_sf, "w")
-    dev = x.device
-    if Kp != _up(K, 128) or w_q.device != dev:
-        raise ValueError(f"x of {K} columns does not fit weights of {Kp} codes on {w_q.device}")
-    out_dtype = out_dtype or x.dtype
-    t = _type(out_dtype, "out_dtype")
-    out = torch.empty((M, N), dtype=out_dtype, device=dev)
+    xt, M, K, ldx, wp, wsp, N, index, out_dtype, t = _weights(x, w_q, w_sf, out_dtype, False)
+    out = x.new_empty((M, N), dtype=out_dtype)
     L = lib()
     n = L.nvfp4_mx_linear_workspace(M, N, K)
-    ws = _workspace(n, dev)
-    _check(L.nvfp4_mx_linear(_ptr(x), _TYPES[x.dtype], M, K, ldx, _ptr(w_q), _ptr(w_sf), N, t, _ptr(out), _ptr(ws), n,
-                             _stream(dev)))
+    ws = _workspace(x, n)
+    st = L.nvfp4_mx_linear(x.data_ptr(), xt, M, K, ldx, wp, wsp, N, t, out.data_ptr(),
+                           None if ws is None else ws.data_ptr(), n, _stream(index))
+    if st:
+        _check(st)
     return out
 
 
@@ -226,23 +255,14 @@ def mx_linear_grouped(x: torch.Tensor, w_q, w_sf, offsets, rows=None, row_scale=
                       out_dtype=None) -> torch.Tensor:
     """:func:`mx_gemm_grouped` on x [M, K], each of its rows cast once on the
     way: out[r] = row_scale[r] * Q(x[rows[r]]) W_e^T for the rows r of e."""
-    ldx = _matrix(x)
-    M, K = x.shape
-    N, Kp = _codes(w_q, w_sf, "w", batch=True)
-    dev = x.device
-    if Kp != _up(K, 128) or w_q.device != dev:
-        raise ValueError(f"x of {K} columns does not fit weights of {Kp} codes on {w_q.device}")
-    E, R = _groups(offsets, rows, M, dev)
-    if E != w_q.shape[0]:
-        raise ValueError(f"offsets are for {E} groups, w for {w_q.shape[0]}")
-    if row_scale is not None:
-        _tensor(row_scale, torch.float32, dev, "row_scale", (R,))
-    out_dtype = out_dtype or x.dtype
-    t = _type(out_dtype, "out_dtype")
-    out = torch.empty((R, N), dtype=out_dtype, device=dev)
+    xt, M, K, ldx, wp, wsp, N, index, out_dtype, t = _weights(x, w_q, w_sf, out_dtype, True)
+    op, rp, E, R, fp = _grouped_shapes(offsets, rows, row_scale, M, w_q.shape[0], index, "w")
+    out = x.new_empty((R, N), dtype=out_dtype)
     L = lib()
     n = L.nvfp4_mx_linear_grouped_workspace(M, R, N, K)
-    ws = _workspace(n, dev)
-    _check(L.nvfp4_mx_linear_grouped(_ptr(x), _TYPES[x.dtype], M, K, ldx, _ptr(rows), R, _ptr(offsets), E, _ptr(w_q),
-                                     _ptr(w_sf), N, _ptr(row_scale), t, _ptr(out), _ptr(ws), n, _stream(dev)))
+    ws = _workspace(x, n)
+    st = L.nvfp4_mx_linear_grouped(x.data_ptr(), xt, M, K, ldx, rp, R, op, E, wp, wsp, N, fp, t, out.data_ptr(),
+                                   None if ws is None else ws.data_ptr(), n, _stream(index))
+    if st:
+        _check(st)
     return out
