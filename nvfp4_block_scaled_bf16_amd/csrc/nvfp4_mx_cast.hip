@@ -72,8 +72,11 @@ __global__ __launch_bounds__(256) void k_mx_rows(MxCast c, uint32_t nchunk) {
 // either direction, so x is read once.  Wave w has rows 32 w .. 32 w + 31 and
 // a lane two adjacent columns: a column's block of 32 rows is within the lane
 // (its maximum and its 16 code bytes need no exchange), and a row's block of
-// 32 columns is 16 lanes, whose maximum is four rotations inside a DPP row.
-// Codes go through LDS only to leave in whole 64-byte runs.
+// 32 columns is 16 lanes.  The 32 rows' maxima are reduced and spread over the
+// lanes at once, two rows to a register, halving what a lane holds with each of
+// four exchanges, so that lane i ends with rows 2 i and 2 i + 1 and computes
+// their codes alone; the lanes read the 32 codes back from LDS.  Codes go
+// through LDS to leave in whole 64-byte runs.
 template <int T>
 struct Two {
     uint32_t w[T == MX_F32 ? 2 : 1];
@@ -93,13 +96,26 @@ __device__ __forceinline__ Two<T> load_two(const char* p, int valid) {
     return v;
 }
 
+// two 16-bit magnitudes that order as the elements' do and keep their exponents
+// (fp32: the upper halves)
 template <int T>
-__device__ __forceinline__ uint32_t two_mag(const Two<T>& v) {
-    if constexpr (T == MX_F32) {
-        const uint32_t a = v.w[0] & 0x7fffffffu, b = v.w[1] & 0x7fffffffu;
-        return a > b ? a : b;
-    } else {
-        return max_halves(abs2(v.w[0]));
+__device__ __forceinline__ uint32_t two_mags(const Two<T>& v) {
+    if constexpr (T == MX_F32) return abs2(__builtin_amdgcn_perm(v.w[1], v.w[0], 0x07060302u));
+    else return abs2(v.w[0]);
+}
+template <int T>
+__device__ __forceinline__ uint32_t scale_code16(uint32_t m16) {
+    return mx_scale_code(T == MX_F32 ? m16 << 16 : mx_mag_bits<T>(m16));
+}
+
+// maximum with the partner lane (DPP pattern CTRL), half of the values kept on
+// either side: v[i] of lanes with `upper` clear, v[i + H] of those with it set
+template <int CTRL, int H>
+__device__ __forceinline__ void max_scatter(uint32_t* v, bool upper) {
+#pragma unroll
+    for (int i = 0; i < H; ++i) {
+        const uint32_t keep = upper ? v[i + H] : v[i], send = upper ? v[i] : v[i + H];
+        v[i] = pk_max_u16(keep, mx_dpp<CTRL>(send));
     }
 }
 
@@ -121,7 +137,7 @@ constexpr int kColPitch = 20;   // words per column's 64 code bytes in LDS: 16-b
 struct TileLds {
     uint32_t colq[128 * kColPitch];
     uint32_t rowq[4][8][64];      // [wave][rows 4 g .. 4 g + 3][lane]: one byte per row
-    uint8_t rsf[128][4];
+    uint8_t rsf[4][4][32];        // [wave][block][row]
     uint8_t csf[128][4];
 };
 
@@ -164,23 +180,16 @@ __global__ __launch_bounds__(256) void k_mx_tile(MxCast c, uint32_t nkt, int64_t
     }
 
     // columns: this wave's 32 rows are one block of each of the lane's two
-    uint32_t m0 = 0, m1 = 0;
-    if constexpr (T == MX_F32) {
+    uint32_t mm[16], mc = 0;
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-            const uint32_t a = v[i].w[0] & 0x7fffffffu, b = v[i].w[1] & 0x7fffffffu;
-            m0 = a > m0 ? a : m0;
-            m1 = b > m1 ? b : m1;
-        }
-    } else {
-        uint32_t m = 0;
-#pragma unroll
-        for (int i = 0; i < 32; ++i) m = pk_max_u16(m, abs2(v[i].w[0]));
-        m0 = m & 0xffffu;
-        m1 = m >> 16;
+    for (int r = 0; r < 16; ++r) {
+        const uint32_t a = two_mags<T>(v[2 * r]), b = two_mags<T>(v[2 * r + 1]);
+        mc = pk_max_u16(mc, pk_max_u16(a, b));
+        // rows 2 r and 2 r + 1 over the two columns
+        mm[r] = pk_max_u16(__builtin_amdgcn_perm(b, a, 0x05040100u), __builtin_amdgcn_perm(b, a, 0x07060302u));
     }
     {
-        const uint32_t k0 = mx_scale_code(mx_mag_bits<T>(m0)), k1 = mx_scale_code(mx_mag_bits<T>(m1));
+        const uint32_t k0 = scale_code16<T>(mc & 0xffffu), k1 = scale_code16<T>(mc >> 16);
         const float s0 = mx_cvt_scale(k0), s1 = mx_cvt_scale(k1);
         u32x4 q0, q1;
 #pragma unroll
@@ -201,33 +210,27 @@ __global__ __launch_bounds__(256) void k_mx_tile(MxCast c, uint32_t nkt, int64_t
     }
 
     if constexpr (ROW) {
-        uint32_t keep0 = 0, keep1 = 0;
+        max_scatter<0x140, 8>(mm, lane & 8);      // row_mirror: lane ^ 15
+        max_scatter<0x141, 4>(mm, lane & 4);      // row_half_mirror: lane ^ 7
+        max_scatter<0x1B, 2>(mm, lane & 2);       // lane ^ 3
+        max_scatter<kDppXor1, 1>(mm, lane & 1);
+        const uint32_t k0 = scale_code16<T>(mm[0] & 0xffffu), k1 = scale_code16<T>(mm[0] >> 16);
+        uint8_t* const mine = S.rsf[wave][lane >> 4];
+        *(uint16_t*)&mine[2 * (lane & 15)] = (uint16_t)(k0 | k1 << 8);
+        __builtin_amdgcn_wave_barrier();
+        uint32_t code[8];
+        *(u32x4*)&code[0] = *(const u32x4*)&mine[0];
+        *(u32x4*)&code[4] = *(const u32x4*)&mine[16];
 #pragma unroll
         for (int g = 0; g < 8; ++g) {
-            uint32_t code[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int i = 4 * g + j;
-                uint32_t m = two_mag<T>(v[i]), o;
-                o = mx_dpp<kDppRor8>(m);
-                m = o > m ? o : m;
-                o = mx_dpp<kDppRor4>(m);
-                m = o > m ? o : m;
-                o = mx_dpp<kDppRor2>(m);
-                m = o > m ? o : m;
-                o = mx_dpp<kDppRor1>(m);
-                m = o > m ? o : m;
-                code[j] = mx_scale_code(mx_mag_bits<T>(m));
-                if (i < 16) keep0 = (lane & 15) == i ? code[j] : keep0;
-                else keep1 = (lane & 15) == i - 16 ? code[j] : keep1;
-            }
-            uint32_t q = put_row<T, 0>(0u, v[4 * g], mx_cvt_scale(code[0]));
-            q = put_row<T, 1>(q, v[4 * g + 1], mx_cvt_scale(code[1]));
-            q = put_row<T, 2>(q, v[4 * g + 2], mx_cvt_scale(code[2]));
-            S.rowq[wave][g][lane] = put_row<T, 3>(q, v[4 * g + 3], mx_cvt_scale(code[3]));
+            // code byte j of the word, in the exponent's place (a NaN block's codes are unspecified)
+            const float s0 = __uint_as_float((code[g] << 23) & 0x7f800000u), s1 = __uint_as_float((code[g] << 15) & 0x7f800000u);
+            const float s2 = __uint_as_float((code[g] << 7) & 0x7f800000u), s3 = __uint_as_float((code[g] >> 1) & 0x7f800000u);
+            uint32_t q = put_row<T, 0>(0u, v[4 * g], s0);
+            q = put_row<T, 1>(q, v[4 * g + 1], s1);
+            q = put_row<T, 2>(q, v[4 * g + 2], s2);
+            S.rowq[wave][g][lane] = put_row<T, 3>(q, v[4 * g + 3], s3);
         }
-        S.rsf[32 * wave + (lane & 15)][lane >> 4] = (uint8_t)keep0;
-        S.rsf[32 * wave + 16 + (lane & 15)][lane >> 4] = (uint8_t)keep1;
     }
     __syncthreads();
 
@@ -255,8 +258,12 @@ __global__ __launch_bounds__(256) void k_mx_tile(MxCast c, uint32_t nkt, int64_t
             }
         }
         // without groups the tile's rows are a whole scale tile, codes past R are 0
-        if (tid < (GROUPED ? nrow : 128))
-            *(uint32_t*)(c.row_sf + mx_sf_offset(r0 + tid, kt, nkt)) = *(const uint32_t*)S.rsf[tid];
+        if (tid < (GROUPED ? nrow : 128)) {
+            const uint8_t(*const f)[32] = S.rsf[tid >> 5];
+            const int row = tid & 31;
+            *(uint32_t*)(c.row_sf + mx_sf_offset(r0 + tid, kt, nkt)) =
+                (uint32_t)f[0][row] | (uint32_t)f[1][row] << 8 | (uint32_t)f[2][row] << 16 | (uint32_t)f[3][row] << 24;
+        }
     }
 }
 
