@@ -31,6 +31,13 @@ constexpr int kMxStep = 128;                // elements of K per scale word
 // workgroups of one launch, in one grid dimension
 constexpr int64_t kMxMaxGrid = (int64_t(1) << 31) - 1;
 
+// The workgroups of a launch go to the 8 XCDs in turn; each XCD takes a
+// contiguous run of tiles, so that its L2 holds the operand rows they share.
+__device__ __forceinline__ uint32_t xcd_index() {
+    const uint32_t g = gridDim.x, x = blockIdx.x & 7u, i = blockIdx.x >> 3;
+    return x * (g >> 3) + (x < (g & 7u) ? x : (g & 7u)) + i;
+}
+
 // byte offset of the scale word of vector r, 128-element step kt
 __device__ __forceinline__ int64_t mx_sf_offset(int64_t r, int64_t kt, int64_t Kt) {
     return (((r >> 7) * Kt + kt) * 128 + (r & 127)) * 4;

@@ -124,7 +124,9 @@ nvfp4_status nvfp4_mx_dequantize(const uint8_t* q, const uint8_t* sf, int64_t R,
         (s = check_count(C, kMaxRows, "C")) != NVFP4_OK)
         return s;
     if (R == 0 || C == 0) return ok();
-    if ((s = check_operand(q, sf, "mx")) != NVFP4_OK || (s = check_output(out, out_type)) != NVFP4_OK) return s;
+    if ((s = check_operand(q, sf, "mx")) != NVFP4_OK || (s = check_output(out, out_type)) != NVFP4_OK ||
+        (s = check_grid(up(R, 4) / 4, up(C, 512) / 512, "mx dequantize")) != NVFP4_OK)
+        return s;
     return (s = check_hip(launch_mx_dequant(q, sf, R, C, out_type, out, as_stream(stream)), "mx dequantize")) != NVFP4_OK
                ? s
                : ok();

@@ -132,13 +132,14 @@ __device__ __forceinline__ uint32_t put_col(uint32_t old, const Two<T>& a, const
     else return mx_put16<T, SEL>(old, __builtin_amdgcn_perm(b.w[0], a.w[0], COL ? 0x07060302u : 0x05040100u), scale);
 }
 
-constexpr int kColPitch = 20;   // words per column's 64 code bytes in LDS: 16-byte aligned, off the banks' period
-
+template <int W>
 struct TileLds {
+    // words per column's 16 W code bytes: 16-byte aligned, off the banks' period
+    static constexpr int kColPitch = 4 * W + 4;
     uint32_t colq[128 * kColPitch];
-    uint32_t rowq[4][8][64];      // [wave][rows 4 g .. 4 g + 3][lane]: one byte per row
-    uint8_t rsf[4][4][32];        // [wave][block][row]
-    uint8_t csf[128][4];
+    uint32_t rowq[W][8][64];      // [wave][rows 4 g .. 4 g + 3][lane]: one byte per row
+    uint8_t rsf[W][4][32];        // [wave][block][row]
+    uint8_t csf[128][W];
 };
 
 // bytes j of four words -> word j (a 4 x 4 byte transpose)
@@ -151,20 +152,22 @@ __device__ __forceinline__ void transpose4(const uint32_t* w, uint32_t* o) {
     o[3] = __builtin_amdgcn_perm(d, b, 0x07060302u);
 }
 
-template <int T, bool ROW, bool GROUPED>
-__global__ __launch_bounds__(256) void k_mx_tile(MxCast c, uint32_t nkt, int64_t Tt) {
+template <int T, bool ROW, bool GROUPED, int W>
+__global__ __launch_bounds__(64 * W) void k_mx_tile(MxCast c, uint32_t nkt, int64_t Tt) {
+    static_assert(W == 4 || !GROUPED, "a group's tiles are one 128-element step");
     constexpr int B = T == MX_F32 ? 4 : 2;
-    __shared__ __attribute__((aligned(16))) TileLds S;
+    constexpr int kColPitch = TileLds<W>::kColPitch;
+    __shared__ __attribute__((aligned(16))) TileLds<W> S;
     const int tid = (int)threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int64_t mt = blockIdx.x / nkt, kt = blockIdx.x % nkt;
-    int64_t r0 = mt * 128, rend = c.R;
+    int64_t r0 = mt * (32 * W), rend = c.R;
     if constexpr (GROUPED) {
         const MxGroupTile g = mx_find_group(c.offsets, c.E, c.R, 128, mt);
         if (g.e < 0) return;
         r0 = g.begin;
         rend = g.end;
     }
-    const int nrow = (int)(rend - r0 < 128 ? rend - r0 : 128);   // >= 1
+    const int nrow = (int)(rend - r0 < 32 * W ? rend - r0 : 32 * W);   // >= 1
     const int64_t c0 = kt * 128 + 2 * lane, left = c.K - c0;
     const int valid = left >= 2 ? 2 : (left > 0 ? 1 : 0);
 
@@ -235,18 +238,24 @@ __global__ __launch_bounds__(256) void k_mx_tile(MxCast c, uint32_t nkt, int64_t
     __syncthreads();
 
     if (c.col_q) {
+        // runs of 16 W bytes of a column; past the last 128 rows there is nothing
+        const int64_t run = (int64_t)(W / 4) * 64 * mt, end = Tt * 64;
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            const int id = tid + 256 * j, col = id >> 2, part = id & 3;
-            if (kt * 128 + col < c.K)
-                *(u32x4*)(c.col_q + ((kt * 128 + col) * Tt + mt) * 64 + 16 * part) = *(const u32x4*)&S.colq[col * kColPitch + 4 * part];
+            const int id = tid + 64 * W * j, col = id / W, part = id % W;
+            if (kt * 128 + col < c.K && run + 16 * part < end)
+                *(u32x4*)(c.col_q + (kt * 128 + col) * end + run + 16 * part) = *(const u32x4*)&S.colq[col * kColPitch + 4 * part];
         }
-        if (tid < 128) *(uint32_t*)(c.col_sf + ((kt * Tt + mt) * 128 + tid) * 4) = *(const uint32_t*)S.csf[tid];
+        if (tid < 32 * W) {
+            const int64_t step = (W / 4) * mt + tid / 128;
+            if (step < Tt)
+                *(uint32_t*)(c.col_sf + ((kt * Tt + step) * 128 + tid % 128) * 4) = *(const uint32_t*)&S.csf[tid % 128][4 * (tid / 128)];
+        }
     }
     if constexpr (ROW) {
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            const int id = tid + 256 * j, w = id >> 7, g = (id >> 4) & 7, p = id & 15;
+            const int id = tid + 64 * W * j, w = id >> 7, g = (id >> 4) & 7, p = id & 15;
             const u32x4 in = *(const u32x4*)&S.rowq[w][g][4 * p];
             const uint32_t a[4] = {in.x, in.y, in.z, in.w};
             uint32_t o[4];
@@ -257,8 +266,9 @@ __global__ __launch_bounds__(256) void k_mx_tile(MxCast c, uint32_t nkt, int64_t
                 if (row < nrow) *(uint32_t*)(c.row_q + ((r0 + row) * nkt + kt) * 64 + 4 * p) = o[i];
             }
         }
-        // without groups the tile's rows are a whole scale tile, codes past R are 0
-        if (tid < (GROUPED ? nrow : 128)) {
+        // without groups the tile's rows fill whole scale tiles, codes past R are 0
+        const int64_t pad = (c.R + 127) / 128 * 128 - r0;
+        if (tid < (GROUPED ? nrow : (pad < 32 * W ? (int)pad : 32 * W))) {
             const uint8_t(*const f)[32] = S.rsf[tid >> 5];
             const int row = tid & 31;
             *(uint32_t*)(c.row_sf + mx_sf_offset(r0 + tid, kt, nkt)) =
@@ -274,36 +284,49 @@ __device__ __forceinline__ float scale_value(uint32_t c) {
     return c == 255u ? __uint_as_float(0x7fc00000u) : (c ? __uint_as_float(c << 23) : 0x1p-127f);
 }
 
-// A thread takes 8 elements: one word of codes, 16 or 32 bytes out.  Grid
-// magnitude times a power of two is exact in fp32 except below 2^-149, which
-// no code reaches (0.5 * 2^-127 = 2^-128).
-template <int T>
+// A wave takes RPW rows by 512 columns, 8 elements a lane: one word of codes, a
+// scale byte, 16 or 32 bytes out.  Grid magnitude times a power of two is exact
+// in fp32 except below 2^-149, which no code reaches (0.5 * 2^-127 = 2^-128).
+template <int T, int RPW>
 __global__ __launch_bounds__(256) void k_mx_dequant(const uint8_t* __restrict__ q, const uint8_t* __restrict__ sf,
-                                                    int64_t R, int64_t C, char* __restrict__ out) {
-    const int64_t per = (C + 7) / 8, n = R * per, Kt = (C + kMxStep - 1) / kMxStep;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
-        const int64_t r = i / per, c0 = (i - r * per) * 8;
-        const uint32_t w = *(const uint32_t*)(q + r * (Kt * 64) + c0 / 2);
-        const float s = scale_value(sf[mx_sf_offset(r, c0 >> 7, Kt) + ((c0 >> 5) & 3)]);
+                                                    int64_t R, int64_t C, char* __restrict__ out, uint32_t nchunk) {
+    const int lane = (int)(threadIdx.x & 63), wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    const int64_t r0 = ((int64_t)(blockIdx.x / nchunk) * 4 + wave) * RPW;
+    const int64_t c0 = (int64_t)(blockIdx.x % nchunk) * kRowCols + 8 * lane, left = C - c0;
+    const int64_t Kt = (C + kMxStep - 1) / kMxStep;
+    if (left <= 0) return;
+    uint32_t w[RPW], code[RPW];
+#pragma unroll
+    for (int i = 0; i < RPW; ++i) {
+        const int64_t r = r0 + i < R ? r0 + i : R - 1;
+        w[i] = *(const uint32_t*)(q + r * (Kt * 64) + c0 / 2);
+        code[i] = sf[mx_sf_offset(r, c0 >> 7, Kt) + ((c0 >> 5) & 3)];
+    }
+#pragma unroll
+    for (int i = 0; i < RPW; ++i) {
+        const int64_t r = r0 + i;
+        if (r >= R) break;
+        const float s = scale_value(code[i]);
         float v[8];
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
             typedef float f32x2 __attribute__((ext_vector_type(2)));
             f32x2 g;
-            if (b == 0) g = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 0);
-            else if (b == 1) g = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 1);
-            else if (b == 2) g = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 2);
-            else g = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 3);
+            if (b == 0) g = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[i], 1.0f, 0);
+            else if (b == 1) g = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[i], 1.0f, 1);
+            else if (b == 2) g = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[i], 1.0f, 2);
+            else g = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[i], 1.0f, 3);
             v[2 * b] = g.x * s;
             v[2 * b + 1] = g.y * s;
         }
-        const int64_t left = C - c0;
         if constexpr (T == MX_F32) {
             char* o = out + (r * C + c0) * 4;
             if (left >= 8) {
                 __builtin_memcpy(o, v, 32);
             } else {
-                for (int k = 0; k < (int)left; ++k) ((float*)o)[k] = v[k];
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    if (k < left) ((float*)o)[k] = v[k];
             }
         } else {
             uint32_t p[4];
@@ -349,15 +372,30 @@ hipError_t launch_cast(const MxCast& c, hipStream_t st) {
     }
     const int64_t Tt = c.offsets ? mx_max_tiles(c.R, c.E, 128) : (c.R + 127) / 128;
     if (Tt * Kt > kMxMaxGrid) return hipErrorInvalidValue;
-    const dim3 grid((unsigned)(Tt * Kt));
     const uint32_t nkt = (uint32_t)Kt;
+    const dim3 grid((unsigned)(Tt * Kt)), grid8((unsigned)((Tt + 1) / 2 * Kt));
+    const bool tall = Tt * Kt >= 2 * 256;
     if (c.offsets) {
-        if (c.row_q) k_mx_tile<T, true, true><<<grid, 256, 0, st>>>(c, nkt, Tt);
-        else k_mx_tile<T, false, true><<<grid, 256, 0, st>>>(c, nkt, Tt);
+        if (c.row_q) k_mx_tile<T, true, true, 4><<<grid, 256, 0, st>>>(c, nkt, Tt);
+        else k_mx_tile<T, false, true, 4><<<grid, 256, 0, st>>>(c, nkt, Tt);
+    } else if (tall) {
+        if (c.row_q) k_mx_tile<T, true, false, 8><<<grid8, 512, 0, st>>>(c, nkt, Tt);
+        else k_mx_tile<T, false, false, 8><<<grid8, 512, 0, st>>>(c, nkt, Tt);
     } else {
-        if (c.row_q) k_mx_tile<T, true, false><<<grid, 256, 0, st>>>(c, nkt, Tt);
-        else k_mx_tile<T, false, false><<<grid, 256, 0, st>>>(c, nkt, Tt);
+        if (c.row_q) k_mx_tile<T, true, false, 4><<<grid, 256, 0, st>>>(c, nkt, Tt);
+        else k_mx_tile<T, false, false, 4><<<grid, 256, 0, st>>>(c, nkt, Tt);
     }
+    return hipGetLastError();
+}
+
+template <int T>
+hipError_t launch_dequant(const uint8_t* q, const uint8_t* sf, int64_t R, int64_t C, void* out, hipStream_t st) {
+    const int64_t chunks = (C + kRowCols - 1) / kRowCols;
+    const int rpw = R * chunks >= 4 * 2048 ? 4 : 1;
+    const int64_t grid = chunks * ((R + 4 * rpw - 1) / (4 * rpw));
+    if (grid > kMxMaxGrid) return hipErrorInvalidValue;
+    if (rpw == 4) k_mx_dequant<T, 4><<<(unsigned)grid, 256, 0, st>>>(q, sf, R, C, (char*)out, (uint32_t)chunks);
+    else k_mx_dequant<T, 1><<<(unsigned)grid, 256, 0, st>>>(q, sf, R, C, (char*)out, (uint32_t)chunks);
     return hipGetLastError();
 }
 
@@ -373,12 +411,9 @@ hipError_t launch_mx_cast(const MxCast& c, hipStream_t st) {
 hipError_t launch_mx_dequant(const uint8_t* q, const uint8_t* sf, int64_t R, int64_t C, int type, void* out,
                              hipStream_t st) {
     if (R <= 0 || C <= 0) return hipSuccess;
-    const int64_t blocks = (R * ((C + 7) / 8) + 255) / 256;
-    const dim3 grid((unsigned)(blocks < 256 * 1024 ? blocks : 256 * 1024));
-    if (type == MX_F32) k_mx_dequant<MX_F32><<<grid, 256, 0, st>>>(q, sf, R, C, (char*)out);
-    else if (type == MX_BF16) k_mx_dequant<MX_BF16><<<grid, 256, 0, st>>>(q, sf, R, C, (char*)out);
-    else k_mx_dequant<MX_F16><<<grid, 256, 0, st>>>(q, sf, R, C, (char*)out);
-    return hipGetLastError();
+    if (type == MX_F32) return launch_dequant<MX_F32>(q, sf, R, C, out, st);
+    if (type == MX_BF16) return launch_dequant<MX_BF16>(q, sf, R, C, out, st);
+    return launch_dequant<MX_F16>(q, sf, R, C, out, st);
 }
 
 }  // namespace nvfp4

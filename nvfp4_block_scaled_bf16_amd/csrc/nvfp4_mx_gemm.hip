@@ -78,13 +78,6 @@ __device__ __forceinline__ void load4_to_lds(const uint8_t* src, void* dst) {
     __builtin_amdgcn_global_load_lds((GlobalPtr)src, (LdsPtr)dst, 4, 0, 0);
 }
 
-// The workgroups of a launch go to the 8 XCDs in turn; each XCD takes a
-// contiguous run of tiles, so that its L2 holds the operand rows they share.
-__device__ __forceinline__ uint32_t xcd_index() {
-    const uint32_t g = gridDim.x, x = blockIdx.x & 7u, i = blockIdx.x >> 3;
-    return x * (g >> 3) + (x < (g & 7u) ? x : (g & 7u)) + i;
-}
-
 // Tile t of ntm x ntn in bands of kBand rows of tiles, down a band's tiles of
 // one column and then the next: the 32 tiles that an XCD works on at a time
 // share 8 tiles of a and 4 of b.
