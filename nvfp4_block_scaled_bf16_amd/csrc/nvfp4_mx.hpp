@@ -174,36 +174,80 @@ __device__ __forceinline__ void mx_group_rows(const int32_t* offsets, int e, int
     *end = b;
 }
 
-// The group of tile t when group e has cdiv(rows, unit) tiles, in order.
-// Called by whole waves; every lane gets the answer.  64 groups a step: an
-// inclusive scan over the lanes, then the first lane whose sum passes t.
-__device__ __forceinline__ MxGroupTile mx_find_group(const int32_t* __restrict__ offsets, int E, int64_t R,
-                                                     int unit, int64_t t) {
-    const int lane = (int)(threadIdx.x & 63);
-    int64_t base = 0;
-    for (int e0 = 0; e0 < E; e0 += 64) {
-        int64_t a = 0, b = 0;
-        if (e0 + lane < E) mx_group_rows(offsets, e0 + lane, R, &a, &b);
-        const int n = (int)(b - a + unit - 1) / unit;
-        // inclusive scan: within rows of 16 lanes, then over the rows
-        int s = n;
+// Groups in tiles of `unit` rows, cdiv(rows, unit) each, in order.  Used by
+// whole waves, every lane gets the answers.  Lane l has group base + l of the 64
+// that were scanned last; with at most 64 groups they are scanned once.
+struct MxGroupScan {
+    const int32_t* offsets;
+    int64_t R;
+    int E, unit;
+    int total;              // tiles in all
+    int a, b, n, s;         // this lane's group: rows, tiles, tiles up to its end (from the scan's base)
+
+    __device__ __forceinline__ void scan(int base) {
+        const int lane = (int)(threadIdx.x & 63);
+        int64_t ra = 0, rb = 0;
+        if (base + lane < E) mx_group_rows(offsets, base + lane, R, &ra, &rb);
+        a = (int)ra;
+        b = (int)rb;
+        n = (int)(((uint32_t)(b - a) + (uint32_t)(unit - 1)) / (uint32_t)unit);
+        // inclusive: within rows of 16 lanes, then over the rows
+        s = n;
         s += mx_dpp_or_0<0x111, 0xf>(s);    // row_shr 1, 2, 4, 8
         s += mx_dpp_or_0<0x112, 0xf>(s);
         s += mx_dpp_or_0<0x114, 0xf>(s);
         s += mx_dpp_or_0<0x118, 0xf>(s);
         s += mx_dpp_or_0<0x142, 0xa>(s);    // lane 15 of rows 0 and 2 to rows 1 and 3
         s += mx_dpp_or_0<0x143, 0xc>(s);    // lane 31 to rows 2 and 3
-        const uint64_t past = __ballot(base + s > t);
-        if (past) {
-            const int l = __builtin_ctzll(past);
-            // rows are 31-bit, held to R
-            const int64_t ga = __builtin_amdgcn_readlane((int)a, l), gb = __builtin_amdgcn_readlane((int)b, l);
-            const int64_t first = base + __builtin_amdgcn_readlane(s - n, l);
-            return MxGroupTile{e0 + l, ga + (t - first) * unit, gb};
-        }
-        base += __builtin_amdgcn_readlane(s, 63);
     }
-    return MxGroupTile{-1, 0, 0};
+    __device__ __forceinline__ int sum() const { return __builtin_amdgcn_readlane(s, 63); }
+
+    __device__ __forceinline__ void init(const int32_t* o, int e, int64_t r, int u) {
+        offsets = o;
+        R = r;
+        E = e;
+        unit = u;
+        total = 0;
+        for (int base = 0; base < E; base += 64) {
+            scan(base);
+            total += sum();
+        }
+    }
+    // the group of tile t < total
+    __device__ __forceinline__ MxGroupTile find(int t) {
+        int before = 0;
+        for (int base = 0; base < E; base += 64) {
+            if (E > 64) scan(base);
+            const uint64_t past = __ballot(before + s > t);
+            if (past) {
+                const int l = __builtin_ctzll(past), first = before + __builtin_amdgcn_readlane(s - n, l);
+                return MxGroupTile{base + l, __builtin_amdgcn_readlane(a, l) + (int64_t)(t - first) * unit,
+                                   __builtin_amdgcn_readlane(b, l)};
+            }
+            before += sum();
+        }
+        return MxGroupTile{-1, 0, 0};
+    }
+    // group e's tiles, and those of the groups before it
+    __device__ __forceinline__ void of(int e, int* tiles, int* before) {
+        *before = 0;
+        if (E > 64) {
+            for (int base = 0; base + 64 <= e; base += 64) {
+                scan(base);
+                *before += sum();
+            }
+            scan(e & ~63);
+        }
+        *tiles = __builtin_amdgcn_readlane(n, e & 63);
+        *before += __builtin_amdgcn_readlane(s - n, e & 63);
+    }
+};
+
+// The group of tile t; e = -1 past the last
+__device__ __forceinline__ MxGroupTile mx_find_group(const int32_t* offsets, int E, int64_t R, int unit, int64_t t) {
+    MxGroupScan g;
+    g.init(offsets, E, R, unit);
+    return t < g.total ? g.find((int)t) : MxGroupTile{-1, 0, 0};
 }
 
 // tiles of `unit` rows that E groups of R rows can need at most

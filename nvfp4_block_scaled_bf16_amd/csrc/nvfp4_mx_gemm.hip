@@ -128,52 +128,138 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_gemm(TileArgs p) {
     // loads a thread issues per stage: of a's codes, b's and the scales
     constexpr int QA = BM * 8 / NT, QB = BN * 8 / NT, SL = (2 * (BM + BN) + NT - 1) / NT, L = QA + QB + SL;
     static_assert(BM * 8 % NT == 0 && BN * 8 % NT == 0 && BM % 64 == 0 && BN % 64 == 0, "");
-    static_assert(WM * WN * kSlab <= ST * (int)sizeof(GemmStage<BM, BN>), "");
+    static_assert(WM * WN * kSlab <= (ST - 1) * (int)sizeof(GemmStage<BM, BN>), "");
     __shared__ __attribute__((aligned(16))) GemmStage<BM, BN> S[ST];
     const int tid = (int)threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int wm = wave / WN, wn = wave % WN, half = lane >> 5, lr = lane & 31;
+    const int wm = wave / WN, wn = wave % WN;
+    // The tiles' loop would have everything that depends on the lane alone kept in
+    // registers throughout; hidden() makes it anew where it is used.
+    auto hidden = [](int v) __attribute__((always_inline)) {
+        asm volatile("" : "+v"(v));
+        return v;
+    };
+    int half, lr;
+    // the places after the first hold the outputs' slabs between two tiles
+    char* const slab = (char*)&S[1] + wave * kSlab;
 
-    int64_t m0, n0, mend = p.M, step0 = 0, steps = p.Kt, out0 = 0;
-    const uint8_t *b_q = p.b_q, *b_sf = p.b_sf;
-    {
-        uint32_t id = xcd_index(), tm, tn;
-        if constexpr (MODE == GEMM_WGRAD) {
-            const uint32_t per = p.ntm * p.ntn;
-            const int e = (int)(id / per);
-            id -= (uint32_t)e * per;
-            // the group's steps in the padded rows follow those of the groups before it
-            int before = 0;
-            for (int e0 = 0; e0 < e; e0 += 64) {
-                int64_t a = 0, b = 0;
-                if (e0 + lane < e) mx_group_rows(p.offsets, e0 + lane, p.R, &a, &b);
-                int n = (int)((b - a + 127) >> 7);
-#pragma unroll
-                for (int d = 32; d; d >>= 1) n += __shfl_xor(n, d, 64);
-                before += n;
-            }
-            int64_t a, b;
-            mx_group_rows(p.offsets, e, p.R, &a, &b);
-            step0 = __builtin_amdgcn_readfirstlane(before);
-            steps = (b - a + 127) >> 7;
-            // offsets that are not in order could ask for more steps than there are
-            if (step0 + steps > p.Kt) steps = p.Kt > step0 ? p.Kt - step0 : 0;
-            out0 = (int64_t)e * p.M * p.N;
-        }
+    // This workgroup's tiles: every XCD has a run of them, which its workgroups
+    // take in turn.
+    MxGroupScan groups;
+    uint32_t ntiles = p.ntm * p.ntn;
+    if constexpr (GROUPED) {
+        groups.init(p.offsets, p.E, p.R, BM);
+        ntiles = (uint32_t)groups.total * p.ntn;
+    }
+    if constexpr (MODE == GEMM_WGRAD) {
+        groups.init(p.offsets, p.E, p.R, kMxStep);
+        ntiles *= (uint32_t)p.E;
+    }
+    const uint32_t x = blockIdx.x & 7u, share = ntiles >> 3, left = ntiles & 7u;
+    uint32_t tile = x * share + (x < left ? x : left), tile_end = tile + share + (x < left ? 1u : 0u);
+    const uint32_t stride = (gridDim.x - x + 7u) >> 3;
+    tile += blockIdx.x >> 3;
+    if (tile >= tile_end) return;
+
+    // Where a tile is, and the sources of this thread's loads: row (tid + NT i)
+    // / 8 of the tile, chunk qc.  Rows past the end repeat the last one, whose
+    // products are not stored.  Grouped rows can be anywhere in a.
+    typedef typename std::conditional<MODE == GEMM_GROUPED_FAR, int64_t, uint32_t>::type AOff;
+    int64_t m0, n0, mend, out0 = 0, steps, nst;
+    const uint8_t *abase, *bbase, *sp[SL];
+    AOff qa[QA];
+    uint32_t qb[QB];
+    int second[SL], sdst[SL];
+    auto setup = [&](uint32_t id) __attribute__((always_inline)) {
+        const int t = hidden(tid), qc = (t & 7) ^ ((t >> 3) & 7);
+        uint32_t tm, tn;
+        int64_t step0 = 0;
+        const uint8_t *b_q = p.b_q, *b_sf = p.b_sf;
+        mend = p.M;
+        steps = p.Kt;
         if constexpr (GROUPED) {
             tn = id % p.ntn;
-            const MxGroupTile g = mx_find_group(p.offsets, p.E, p.R, BM, id / p.ntn);
-            if (g.e < 0) return;
+            const MxGroupTile g = groups.find((int)(id / p.ntn));
             m0 = g.begin;
             mend = g.end;
             b_q += (int64_t)g.e * p.N * p.Kt * 64;
             b_sf += (int64_t)g.e * ((p.N + 127) / 128) * p.Kt * 512;
         } else {
+            if constexpr (MODE == GEMM_WGRAD) {
+                const uint32_t per = p.ntm * p.ntn;
+                const int e = (int)(id / per);
+                id -= (uint32_t)e * per;
+                // the group's steps in the padded rows follow those of the groups before it
+                int n, before;
+                groups.of(e, &n, &before);
+                step0 = before;
+                steps = n;
+                // offsets that are not in order could ask for more steps than there are
+                if (step0 + steps > p.Kt) steps = p.Kt > step0 ? p.Kt - step0 : 0;
+                out0 = (int64_t)e * p.M * p.N;
+            }
             band_tile(id, p.ntm, p.ntn, &tm, &tn);
             m0 = (int64_t)tm * BM;
         }
         n0 = (int64_t)tn * BN;
-    }
+        nst = (steps + 1) >> 1;
+        abase = GROUPED ? p.a_q : p.a_q + (m0 * p.Kt + step0) * 64;
+        bbase = b_q + (n0 * p.Kt + step0) * 64;
+        auto arow = [&](int r) {
+            int64_t row = m0 + r < mend ? m0 + r : mend - 1;
+            if constexpr (GROUPED) {
+                if (p.rows) row = p.rows[row];
+                row = row < 0 ? 0 : (row < p.A ? row : p.A - 1);
+            }
+            return row;
+        };
+#pragma unroll
+        for (int i = 0; i < QA; ++i)
+            qa[i] = (AOff)((arow((t + NT * i) >> 3) - (GROUPED ? 0 : m0)) * (p.Kt * 64) + 16 * qc);
+#pragma unroll
+        for (int i = 0; i < QB; ++i) {
+            const int r = (t + NT * i) >> 3;
+            qb[i] = (uint32_t)(n0 + r < p.N ? r : p.N - 1 - n0) * (uint32_t)(p.Kt * 64) + 16 * qc;
+        }
+        // scale words: the stage's first step's of all rows, then the second's
+        // (waves left over bring some again)
+#pragma unroll
+        for (int i = 0; i < SL; ++i) {
+            const int first = (64 * wave + NT * i) % (2 * (BM + BN)), w = first >= BM + BN, f = first - w * (BM + BN), r = f + (t & 63);
+            const int64_t row = f < BM ? arow(r) : (n0 + r - BM < p.N ? n0 + r - BM : p.N - 1);
+            sp[i] = (f < BM ? p.a_sf : b_sf) + mx_sf_offset(row, step0, p.Kt);
+            second[i] = w ? 512 : 0;
+            sdst[i] = first;
+        }
+    };
+    // load n of L of stage k; an odd last step's stage takes it twice, the second
+    // time as zeros
+    const uint32_t back = (uint32_t)((tid ^ (tid >> 3)) & 4) * 16;
+    auto bring = [&](int n, int64_t k, GemmStage<BM, BN>& st) __attribute__((always_inline)) {
+        const bool cut = 2 * k + 1 >= steps;
+        const uint32_t bb = cut ? back : 0u;
+        if (n < QA) {
+            load16_to_lds(abase + k * 128 + (qa[n] - bb), &st.q[16 * (64 * wave + NT * n)]);
+        } else if (n < QA + QB) {
+            load16_to_lds(bbase + k * 128 + (qb[n - QA] - bb), &st.q[128 * BM + 16 * (64 * wave + NT * (n - QA))]);
+        } else {
+            const int i = n - QA - QB;
+            load4_to_lds(sp[i] + k * 1024 + (cut ? 0 : second[i]), &st.sf[0][sdst[i]]);
+        }
+    };
+    // past the last stage its loads come again, into a place that nobody reads
+    auto clamped = [&](int64_t k) { return k < nst ? k : nst - 1; };
+    // A stage's loads begin in the last quarter of the stage ST before it, whose
+    // place it takes, and end a quarter on.
+    constexpr int L1 = L / 2;
 
+    setup(tile);
+    if (steps > 0) {
+#pragma unroll
+        for (int n = 0; n < L; ++n) bring(n, 0, S[0]);
+    }
+  while (true) {
+    half = hidden(lane) >> 5;
+    lr = hidden(lane) & 31;
     f32x16 acc[FM][FN];
 #pragma unroll
     for (int i = 0; i < FM; ++i)
@@ -183,60 +269,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_gemm(TileArgs p) {
             for (int a = 0; a < 16; ++a) acc[i][j][a] = 0.0f;
 
     if (steps > 0) {
-        // Sources of this thread's loads: row (tid + NT i) / 8 of the tile,
-        // chunk qc.  Rows past the end repeat the last one, whose products are
-        // not stored.  Grouped rows can be anywhere in a.
-        constexpr bool GA = GROUPED;
-        typedef typename std::conditional<MODE == GEMM_GROUPED_FAR, int64_t, uint32_t>::type AOff;
-        const uint8_t* const abase = GA ? p.a_q : p.a_q + (m0 * p.Kt + step0) * 64;
-        const uint8_t* const bbase = b_q + (n0 * p.Kt + step0) * 64;
-        auto arow = [&](int r) {
-            int64_t row = m0 + r < mend ? m0 + r : mend - 1;
-            if constexpr (GA) {
-                if (p.rows) row = p.rows[row];
-                row = row < 0 ? 0 : (row < p.A ? row : p.A - 1);
-            }
-            return row;
-        };
-        const int qc = (tid & 7) ^ ((tid >> 3) & 7);
-        AOff qa[QA];
-        uint32_t qb[QB];
-#pragma unroll
-        for (int i = 0; i < QA; ++i)
-            qa[i] = (AOff)((arow((tid + NT * i) >> 3) - (GA ? 0 : m0)) * (p.Kt * 64) + 16 * qc);
-#pragma unroll
-        for (int i = 0; i < QB; ++i) {
-            const int r = (tid + NT * i) >> 3;
-            qb[i] = (uint32_t)(n0 + r < p.N ? r : p.N - 1 - n0) * (uint32_t)(p.Kt * 64) + 16 * qc;
-        }
-        // scale words: the stage's first step's of all rows, then the second's
-        // (waves left over bring some again)
-        const uint8_t* sp[SL];
-        int second[SL], sdst[SL];
-#pragma unroll
-        for (int i = 0; i < SL; ++i) {
-            const int first = (64 * wave + NT * i) % (2 * (BM + BN)), w = first >= BM + BN, f = first - w * (BM + BN), r = f + lane;
-            const int64_t row = f < BM ? arow(r) : (n0 + r - BM < p.N ? n0 + r - BM : p.N - 1);
-            sp[i] = (f < BM ? p.a_sf : b_sf) + mx_sf_offset(row, step0, p.Kt);
-            second[i] = w ? 512 : 0;
-            sdst[i] = first;
-        }
-        const int64_t nst = (steps + 1) >> 1, nfull = steps >> 1;
-        // an odd last step's stage takes it twice, the second time as zeros
-        const uint32_t back = (uint32_t)(qc & 4) * 16;
-        auto bring = [&](int n, int64_t k, GemmStage<BM, BN>& st) __attribute__((always_inline)) {
-            const bool cut = 2 * k + 1 >= steps;
-            const uint32_t bb = cut ? back : 0u;
-            if (n < QA) {
-                load16_to_lds(abase + k * 128 + (qa[n] - bb), &st.q[16 * (64 * wave + NT * n)]);
-            } else if (n < QA + QB) {
-                load16_to_lds(bbase + k * 128 + (qb[n - QA] - bb), &st.q[128 * BM + 16 * (64 * wave + NT * (n - QA))]);
-            } else {
-                const int i = n - QA - QB;
-                load4_to_lds(sp[i] + k * 1024 + (cut ? 0 : second[i]), &st.sf[0][sdst[i]]);
-            }
-        };
-
+        const int64_t nfull = steps >> 1;
         // operand tiles z: b's, then a's
         struct Frags { u32x4 v[FM + FN]; };
         struct Scales { int v[FM + FN]; };
@@ -283,12 +316,9 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_gemm(TileArgs p) {
         using Q3 = std::integral_constant<int, 3>;
         Frags f0, f1;
         Scales sc, sn;
-        // A stage's loads begin in the last quarter of the stage ST before it,
-        // whose place it takes, and end a quarter on
-        constexpr int L1 = L / 2;
-        auto clamped = [&](int64_t k) { return k < nst ? k : nst - 1; };
+        // the first stage is on its way since the last tile
 #pragma unroll
-        for (int u = 0; u < ST; ++u)
+        for (int u = 1; u < ST; ++u)
 #pragma unroll
             for (int n = 0; n < (u + 1 < ST ? L : L1); ++n) bring(n, clamped(u), S[u]);
         asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"((ST - 2) * L + L1) : "memory");
@@ -300,7 +330,6 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_gemm(TileArgs p) {
         // cur: the stage's place; last: that of the stage before it, whose
         // successor's loads end here
         auto stage = [&](int64_t s, GemmStage<BM, BN>& last, GemmStage<BM, BN>& cur, GemmStage<BM, BN>& next) __attribute__((always_inline)) {
-            // past the last stage its loads come again, into a place that nobody reads
             const int64_t k1 = clamped(s + ST - 1), k2 = clamped(s + ST);
             __builtin_amdgcn_sched_barrier(0);
             quarter(Q0{}, f0, sc, f1, cur, 1, nullptr, L1, L, k1, last);
@@ -338,22 +367,35 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_gemm(TileArgs p) {
         asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
     }
 
+    // The next tile's first stage is brought while this one's outputs leave.
+    const int64_t em0 = m0, en0 = n0, eend = mend, eout = out0;
+    tile += stride;
+    const bool more = tile < tile_end;
+    if (more) {
+        setup(tile);
+        if (steps > 0) {
+#pragma unroll
+            for (int n = 0; n < L; ++n) bring(n, 0, S[0]);
+        }
+    }
+
     // Accumulator a of lane l: vector l % 32 of operand a (a row of out), vector
     // 8 (a / 4) + 4 (l / 32) + a % 4 of operand b (a column), of a 32 x 32 block.
     // A wave turns 32 rows at a time around in LDS of its own and stores whole
     // runs of a row.
+    half = hidden(lane) >> 5;
+    lr = hidden(lane) & 31;
     constexpr int WC = BN / WN;
-    char* const slab = (char*)S + wave * kSlab;
-    const int64_t c0 = n0 + wn * WC;
+    const int64_t c0 = en0 + wn * WC;
     const int ncol = (int)(p.N - c0 < WC ? p.N - c0 : WC);
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
-        const int64_t row0 = m0 + wm * (BM / WM) + 32 * i, row = row0 + lr;
-        const int nrow = (int)(mend - row0 < 32 ? mend - row0 : 32);
+        const int64_t row0 = em0 + wm * (BM / WM) + 32 * i, row = row0 + lr;
+        const int nrow = (int)(eend - row0 < 32 ? eend - row0 : 32);
         float f = 1.0f;
         bool zero = false;
         if constexpr (GROUPED) {
-            if (row < mend) {
+            if (row < eend) {
                 if (p.row_scale) f = p.row_scale[row];
                 // a row index outside a stands for a row of zeros
                 if (p.rows && (uint32_t)p.rows[row] >= (uint64_t)p.A) zero = true;
@@ -372,8 +414,8 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_gemm(TileArgs p) {
                         *(f32x4*)&fs[lr * (W + 4) + 32 * (j - j0) + 8 * g + 4 * half] =
                             f32x4{value(j, 4 * g), value(j, 4 * g + 1), value(j, 4 * g + 2), value(j, 4 * g + 3)};
                 __builtin_amdgcn_wave_barrier();
-                store_slab<float, W>(fs, (float*)p.out + out0 + row0 * p.N + c0 + 32 * j0, p.N, nrow, ncol - 32 * j0,
-                                     p.N % 4 == 0 && ((uintptr_t)p.out & 15) == 0, lane);
+                store_slab<float, W>(fs, (float*)p.out + eout + row0 * p.N + c0 + 32 * j0, p.N, nrow, ncol - 32 * j0,
+                                     p.N % 4 == 0 && ((uintptr_t)p.out & 15) == 0, 32 * half + lr);
                 __builtin_amdgcn_wave_barrier();
             }
         } else {
@@ -385,22 +427,30 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_gemm(TileArgs p) {
                     *(u32x2*)&hs[lr * (WC + 8) + 32 * j + 8 * g + 4 * half] =
                         u32x2{pack16(p.type, value(j, 4 * g), value(j, 4 * g + 1)), pack16(p.type, value(j, 4 * g + 2), value(j, 4 * g + 3))};
             __builtin_amdgcn_wave_barrier();
-            store_slab<uint16_t, WC>(hs, (uint16_t*)p.out + out0 + row0 * p.N + c0, p.N, nrow, ncol,
-                                     p.N % 8 == 0 && ((uintptr_t)p.out & 15) == 0, lane);
+            store_slab<uint16_t, WC>(hs, (uint16_t*)p.out + eout + row0 * p.N + c0, p.N, nrow, ncol,
+                                     p.N % 8 == 0 && ((uintptr_t)p.out & 15) == 0, 32 * half + lr);
             __builtin_amdgcn_wave_barrier();
         }
     }
+    if (!more) return;
+    // every wave is done with the slabs, into which later stages come
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  }
 }
 
-template <int BM, int BN, int WM, int WN, int ST, int MODE>
+constexpr int64_t kCus = 256;
+
+template <int BM, int BN, int WM, int WN, int ST, int SLOTS, int MODE>
 hipError_t launch_tiles(TileArgs p, int64_t mtiles, int64_t batch, hipStream_t st) {
     const int64_t ntn = (p.N + BN - 1) / BN;
-    const int64_t grid = mtiles * ntn * batch;
-    if (grid > kMxMaxGrid || mtiles > kMxMaxGrid || ntn > kMxMaxGrid) return hipErrorInvalidValue;
-    if (grid == 0) return hipSuccess;
+    const int64_t tiles = mtiles * ntn * batch;
+    if (tiles > kMxMaxGrid || mtiles > kMxMaxGrid || ntn > kMxMaxGrid) return hipErrorInvalidValue;
+    if (tiles == 0) return hipSuccess;
     p.ntm = (uint32_t)mtiles;
     p.ntn = (uint32_t)ntn;
-    k_mx_gemm<BM, BN, WM, WN, ST, MODE><<<(unsigned)grid, 64 * WM * WN, 0, st>>>(p);
+    // as many workgroups as run at once; each takes several tiles where there are more
+    const int64_t most = kCus * SLOTS;
+    k_mx_gemm<BM, BN, WM, WN, ST, MODE><<<(unsigned)(tiles < most ? tiles : most), 64 * WM * WN, 0, st>>>(p);
     return hipGetLastError();
 }
 
@@ -430,7 +480,7 @@ __global__ __launch_bounds__(64 * W) void k_mx_skinny(SkinnyArgs p) {
     const int tid = (int)threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int lr = lane & 15, g = lane >> 4;
     const TileArgs& t = p.t;
-    const uint32_t id = GROUPED ? xcd_index() : blockIdx.x;
+    const uint32_t id = blockIdx.x;
     const int64_t n0 = (int64_t)(id % t.ntn) * (16 * NT);
     int64_t m0 = (int64_t)(id / t.ntn) * p.unit, mend = t.M;
     const uint8_t *b_q = t.b_q, *b_sf = t.b_sf;
@@ -627,11 +677,9 @@ hipError_t launch_skinny(SkinnyArgs p, int64_t mtiles, hipStream_t st) {
 // (`slots`), per tile (`full`): fits to products of 128 .. 16384 rows, 4096 and
 // 8192 columns and elements.
 struct TileCost { int bm, bn, slots, alone, full; };
-constexpr TileCost kTiles[] = {{256, 256, 1, 700, 700}, {256, 128, 1, 560, 560}, {128, 128, 2, 340, 305},
-                               {64, 128, 2, 228, 193}, {64, 64, 3, 205, 130}};
-constexpr int kNumTiles = 5;
-constexpr int64_t kCus = 256;
-
+constexpr TileCost kTiles[] = {{256, 256, 1, 700, 700}, {128, 128, 2, 340, 305}, {64, 128, 2, 228, 193},
+                               {64, 64, 3, 205, 130}};
+constexpr int kNumTiles = 4;
 // the shape whose `mtiles[i]` rows of tiles by N columns, `batch` times, take the least time
 int best_tile(const int64_t* mtiles, int64_t N, int64_t batch) {
     int best = 0;
@@ -652,11 +700,10 @@ int best_tile(const int64_t* mtiles, int64_t N, int64_t batch) {
 template <int MODE>
 hipError_t launch_best(const TileArgs& p, const int64_t* mtiles, int64_t batch, hipStream_t st) {
     switch (best_tile(mtiles, p.N, batch)) {
-        case 0: return launch_tiles<256, 256, 4, 2, 2, MODE>(p, mtiles[0], batch, st);
-        case 1: return launch_tiles<256, 128, 4, 2, 2, MODE>(p, mtiles[1], batch, st);
-        case 2: return launch_tiles<128, 128, 2, 2, 2, MODE>(p, mtiles[2], batch, st);
-        case 3: return launch_tiles<64, 128, 2, 2, 3, MODE>(p, mtiles[3], batch, st);
-        default: return launch_tiles<64, 64, 2, 2, 3, MODE>(p, mtiles[4], batch, st);
+        case 0: return launch_tiles<256, 256, 4, 2, 2, 1, MODE>(p, mtiles[0], batch, st);
+        case 1: return launch_tiles<128, 128, 2, 2, 2, 2, MODE>(p, mtiles[1], batch, st);
+        case 2: return launch_tiles<64, 128, 2, 2, 3, 2, MODE>(p, mtiles[2], batch, st);
+        default: return launch_tiles<64, 64, 2, 2, 3, 3, MODE>(p, mtiles[3], batch, st);
     }
 }
 
