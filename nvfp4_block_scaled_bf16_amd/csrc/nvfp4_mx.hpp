@@ -31,13 +31,6 @@ constexpr int kMxStep = 128;                // elements of K per scale word
 // workgroups of one launch, in one grid dimension
 constexpr int64_t kMxMaxGrid = (int64_t(1) << 31) - 1;
 
-// The workgroups of a launch go to the 8 XCDs in turn; each XCD takes a
-// contiguous run of tiles, so that its L2 holds the operand rows they share.
-__device__ __forceinline__ uint32_t xcd_index() {
-    const uint32_t g = gridDim.x, x = blockIdx.x & 7u, i = blockIdx.x >> 3;
-    return x * (g >> 3) + (x < (g & 7u) ? x : (g & 7u)) + i;
-}
-
 // byte offset of the scale word of vector r, 128-element step kt
 __device__ __forceinline__ int64_t mx_sf_offset(int64_t r, int64_t kt, int64_t Kt) {
     return (((r >> 7) * Kt + kt) * 128 + (r & 127)) * 4;
@@ -285,9 +278,10 @@ struct MxGemm {
     const float* row_scale;      // optional: factor of row r
 };
 hipError_t launch_mx_gemm(const MxGemm& g, hipStream_t st);
-// whether launch_mx_linear takes this product: x (c) cast on the way, no
-// operand a (g.a_q and g.a_sf unused)
-bool mx_linear_casts(int64_t M, int64_t N, int64_t Kp);
+// whether launch_mx_linear takes this product (or the R grouped rows): x (c)
+// cast on the way, no operand a (g.a_q and g.a_sf unused)
+bool mx_linear_casts(int64_t M, int64_t Kp);
+bool mx_linear_grouped_casts(int64_t R, int64_t Kp);
 hipError_t launch_mx_linear(const MxGemm& g, const MxCast& c, hipStream_t st);
 
 struct MxWgrad {

@@ -189,7 +189,7 @@ nvfp4_status nvfp4_mx_wgrad_grouped(const uint8_t* a_q, const uint8_t* a_sf, con
 
 int64_t nvfp4_mx_linear_workspace(int64_t M, int64_t N, int64_t K) {
     if (M < 0 || N < 0 || K < 0 || M > kMaxRows || N > kMaxRows || K > kMaxK) return 0;
-    if (mx_linear_casts(M, N, up(K, 128))) return 0;
+    if (mx_linear_casts(M, up(K, 128))) return 0;
     return M * (up(K, 128) / 2) + up(M, 128) * (up(K, 128) / 32);
 }
 
@@ -212,7 +212,7 @@ nvfp4_status nvfp4_mx_linear(const void* x, nvfp4_dtype x_type, int64_t M, int64
     uint8_t* q = (uint8_t*)workspace;
     uint8_t* sf = q + M * (up(K, 128) / 2);
     const MxCast c{x, x_type, M, K, ldx, nullptr, M, nullptr, 0, q, sf, nullptr, nullptr};
-    const bool casts = need == 0;
+    const bool casts = mx_linear_casts(M, up(K, 128));
     if (K > 0 && !casts && (s = check_hip(launch_mx_cast(c, as_stream(stream)), "mx cast")) != NVFP4_OK) return s;
     const MxGemm g{q, sf, M, w_q, w_sf, M, N, up(K, 128), out_type, out, nullptr, 0, nullptr, nullptr};
     return (s = check_hip(casts ? launch_mx_linear(g, c, as_stream(stream)) : launch_mx_gemm(g, as_stream(stream)),
@@ -222,9 +222,8 @@ nvfp4_status nvfp4_mx_linear(const void* x, nvfp4_dtype x_type, int64_t M, int64
 }
 
 int64_t nvfp4_mx_linear_grouped_workspace(int64_t M, int64_t R, int64_t N, int64_t K) {
-    (void)R;
-    (void)N;
-    if (M < 0 || K < 0 || M > kMaxRows || K > kMaxK) return 0;
+    if (M < 0 || R < 0 || N < 0 || K < 0 || M > kMaxRows || R > kMaxRows || N > kMaxRows || K > kMaxK) return 0;
+    if (mx_linear_grouped_casts(R, up(K, 128))) return 0;
     return M * (up(K, 128) / 2) + up(M, 128) * (up(K, 128) / 32);
 }
 
@@ -251,12 +250,14 @@ nvfp4_status nvfp4_mx_linear_grouped(const void* x, nvfp4_dtype x_type, int64_t 
     if (!aligned(workspace, 16)) return fail(NVFP4_EALIGN, "workspace must be 16-byte aligned");
     uint8_t* q = (uint8_t*)workspace;
     uint8_t* sf = q + M * (up(K, 128) / 2);
-    if (K > 0) {
-        const MxCast c{x, x_type, M, K, ldx, nullptr, M, nullptr, 0, q, sf, nullptr, nullptr};
-        if ((s = check_hip(launch_mx_cast(c, as_stream(stream)), "mx cast")) != NVFP4_OK) return s;
-    }
+    const MxCast c{x, x_type, M, K, ldx, nullptr, M, nullptr, 0, q, sf, nullptr, nullptr};
+    const bool casts = mx_linear_grouped_casts(R, up(K, 128));
+    if (K > 0 && !casts && (s = check_hip(launch_mx_cast(c, as_stream(stream)), "mx cast")) != NVFP4_OK) return s;
     const MxGemm g{q, sf, M, w_q, w_sf, R, N, up(K, 128), out_type, out, offsets, num_groups, rows, row_scale};
-    return (s = check_hip(launch_mx_gemm(g, as_stream(stream)), "mx grouped gemm")) != NVFP4_OK ? s : ok();
+    return (s = check_hip(casts ? launch_mx_linear(g, c, as_stream(stream)) : launch_mx_gemm(g, as_stream(stream)),
+                          "mx grouped linear")) != NVFP4_OK
+               ? s
+               : ok();
 }
 
 }  // extern "C"

@@ -707,19 +707,18 @@ hipError_t launch_best(const TileArgs& p, const int64_t* mtiles, int64_t batch, 
     }
 }
 
-template <int MT, int IN, bool GROUPED>
+template <int MT>
 hipError_t launch_few_nt(const SkinnyArgs& p, int64_t mtiles, hipStream_t st) {
     // twice the columns to a workgroup where that leaves one for every compute unit
-    if (mtiles * ((p.t.N + 31) / 32) >= kCus) return launch_skinny<MT, 2, 4, IN, GROUPED>(p, mtiles, st);
-    return launch_skinny<MT, 1, 4, IN, GROUPED>(p, mtiles, st);
+    if (mtiles * ((p.t.N + 31) / 32) >= kCus) return launch_skinny<MT, 2, 4, -1, false>(p, mtiles, st);
+    return launch_skinny<MT, 1, 4, -1, false>(p, mtiles, st);
 }
 
-template <bool GROUPED>
-hipError_t launch_few(SkinnyArgs p, int64_t rows, int64_t mtiles, hipStream_t st) {
-    if (rows <= 16) return launch_few_nt<1, -1, GROUPED>(p, mtiles, st);
-    if (rows <= 32) return launch_few_nt<2, -1, GROUPED>(p, mtiles, st);
-    if (rows <= 48) return launch_few_nt<3, -1, GROUPED>(p, mtiles, st);
-    return launch_few_nt<4, -1, GROUPED>(p, mtiles, st);
+hipError_t launch_few(const SkinnyArgs& p, int64_t rows, int64_t mtiles, hipStream_t st) {
+    if (rows <= 16) return launch_few_nt<1>(p, mtiles, st);
+    if (rows <= 32) return launch_few_nt<2>(p, mtiles, st);
+    if (rows <= 48) return launch_few_nt<3>(p, mtiles, st);
+    return launch_few_nt<4>(p, mtiles, st);
 }
 
 // Rows of x that a workgroup can hold as codes (0: too long a row): up to 16,
@@ -736,11 +735,16 @@ constexpr int64_t kFewOutputs = int64_t(1) << 19;
 
 }  // namespace
 
-bool mx_linear_casts(int64_t M, int64_t N, int64_t Kp) {
-    (void)N;
-    const int most = cast_rows(Kp / kMxStep);
-    return M <= (most < 8 ? most : 8);
-}
+// Rows up to which the product casts x itself instead of in a launch before it.
+// Each workgroup casts its own: 1 x 8192 -> 28672 26 us with or without, 8 rows
+// 38 us against 28 and a cast of 3; 32 rows over 64 experts of 4096 x 4096 33 us
+// against 33 and a cast of 3, 64 rows 71 against 66.
+constexpr int64_t kCastDense = 4, kCastGrouped = 32;
+constexpr int kCastUnit = 8;    // rows to a grouped workgroup
+
+bool mx_linear_casts(int64_t M, int64_t Kp) { return M <= kCastDense && cast_rows(Kp / kMxStep) >= M; }
+
+bool mx_linear_grouped_casts(int64_t R, int64_t Kp) { return R <= kCastGrouped && cast_rows(Kp / kMxStep) >= kCastUnit; }
 
 hipError_t launch_mx_gemm(const MxGemm& g, hipStream_t st) {
     if (g.M <= 0 || g.N <= 0) return hipSuccess;
@@ -749,24 +753,31 @@ hipError_t launch_mx_gemm(const MxGemm& g, hipStream_t st) {
     int64_t mtiles[kNumTiles];
     if (g.offsets) {
         for (int i = 0; i < kNumTiles; ++i) mtiles[i] = mx_max_tiles(g.M, g.E, kTiles[i].bm);
-        if (g.A >= (int64_t(1) << 32) / (g.Kp / 2)) return launch_best<GEMM_GROUPED_FAR>(p, mtiles, 1, st);
+        if (g.A * (g.Kp / 2) >= int64_t(1) << 32) return launch_best<GEMM_GROUPED_FAR>(p, mtiles, 1, st);
         return launch_best<GEMM_GROUPED>(p, mtiles, 1, st);
     }
     if (g.M <= kFewOutputs / g.N) {
         const SkinnyArgs s{p, nullptr, g.Kp, 0, g.M <= 64 ? (int)((g.M + 15) / 16 * 16) : 64};
-        return launch_few<false>(s, s.unit, (g.M + s.unit - 1) / s.unit, st);
+        return launch_few(s, s.unit, (g.M + s.unit - 1) / s.unit, st);
     }
     for (int i = 0; i < kNumTiles; ++i) mtiles[i] = (g.M + kTiles[i].bm - 1) / kTiles[i].bm;
     return launch_best<GEMM_DENSE>(p, mtiles, 1, st);
 }
 
+template <int IN>
+hipError_t launch_casting(const SkinnyArgs& s, hipStream_t st) {
+    if (s.t.offsets) return launch_skinny<1, 2, 4, IN, true>(s, mx_max_tiles(s.t.M, s.t.E, s.unit), st);
+    return launch_skinny<1, 1, 4, IN, false>(s, 1, st);
+}
+
 hipError_t launch_mx_linear(const MxGemm& g, const MxCast& c, hipStream_t st) {
+    if (g.M <= 0 || g.N <= 0) return hipSuccess;
     TileArgs p{nullptr, nullptr, g.b_q, g.b_sf, g.A, g.M, g.N, g.Kp / kMxStep, g.out, g.type, g.offsets, g.E, g.M,
                g.rows, g.row_scale, 0, 0};
-    const SkinnyArgs s{p, c.x, c.K, c.ldx, (int)g.M};
-    if (c.type == MX_F32) return launch_skinny<1, 1, 4, MX_F32, false>(s, 1, st);
-    if (c.type == MX_BF16) return launch_skinny<1, 1, 4, MX_BF16, false>(s, 1, st);
-    return launch_skinny<1, 1, 4, MX_F16, false>(s, 1, st);
+    const SkinnyArgs s{p, c.x, c.K, c.ldx, g.offsets ? kCastUnit : (int)g.M};
+    if (c.type == MX_F32) return launch_casting<MX_F32>(s, st);
+    if (c.type == MX_BF16) return launch_casting<MX_BF16>(s, st);
+    return launch_casting<MX_F16>(s, st);
 }
 
 hipError_t launch_mx_wgrad(const MxWgrad& g, hipStream_t st) {

@@ -92,6 +92,12 @@ def test_empty_sums_and_sizes():
     assert nv.mx_gemm(e["row_q"], e["row_sf"], wq, wsf).shape == (0, 5)
     assert nv.mx_gemm(wq, wsf, e["row_q"], e["row_sf"]).shape == (5, 0)
     assert nv.mx_linear(torch.zeros(0, 64, device="cuda"), wq, wsf).shape == (0, 5)
+    for M in (1, 7, 300, 5000):                          # nothing to sum: zeros
+        x = torch.zeros(M, 0, device="cuda")
+        assert torch.equal(nv.mx_linear(x, z["row_q"], z["row_sf"]).cpu(), torch.zeros(M, 4))
+        off = torch.tensor([0, M // 2, M], dtype=torch.int32, device="cuda")
+        got = nv.mx_linear_grouped(x, z["row_q"].expand(2, 4, 0).contiguous(), z["row_sf"].expand(2, 1, 0, 128, 4).contiguous(), off)
+        assert torch.equal(got.cpu(), torch.zeros(M, 4))
 
 
 def grouped_reference(a, b, off, idx=None):
