@@ -174,12 +174,32 @@ __global__ __launch_bounds__(64 * W) void k_mx_tile(MxCast c, uint32_t nkt, int6
     Two<T> v[32];
     int idx = 0;
     if (c.rows) idx = 32 * wave + (lane & 31) < nrow ? c.rows[r0 + 32 * wave + (lane & 31)] : -1;
-#pragma unroll
-    for (int i = 0; i < 32; ++i) {
+    // rows that are not there read row 0 and count as zeros, so that nothing
+    // stands between the loads (the columns' end alone needs a test per lane)
+    const bool whole = kt * 128 + 128 <= c.K;
+    auto source = [&](int i, uint32_t* mask) {
         int64_t src = r0 + 32 * wave + i;
         if (c.rows) src = __builtin_amdgcn_readlane(idx, i);
         const bool have = 32 * wave + i < nrow && src >= 0 && src < c.M;
-        v[i] = load_two<T>((const char*)c.x + (src * c.ldx + c0) * B, have ? valid : 0);
+        *mask = have ? ~0u : 0u;
+        return (const char*)c.x + ((have ? src : 0) * c.ldx + c0) * B;
+    };
+    if (whole) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+            uint32_t mask;
+            const char* const p = source(i, &mask);
+            v[i] = load_two<T>(p, 2);
+#pragma unroll
+            for (auto& w : v[i].w) w &= mask;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+            uint32_t mask;
+            const char* const p = source(i, &mask);
+            v[i] = load_two<T>(p, mask ? valid : 0);
+        }
     }
 
     // columns: this wave's 32 rows are one block of each of the lane's two

@@ -106,18 +106,23 @@ struct TileArgs {
 // fp32 values each, and 16 bytes that keep the rows' banks apart
 constexpr int kSlab = 32 * (256 + 16);
 
-// Rows [row0, row0 + nrow) and columns [col0, col0 + ncol) of out from a slab
-// of W values a row (T: 2- or 4-byte values), by one wave
+// nrow rows and ncol columns of out from a slab of W values a row (T: 2- or
+// 4-byte values), by one wave, 16 bytes to a lane and store.  A row of out need
+// not be aligned to more than its type: the hardware splits what it has to (777
+// x 4095 fp16 outputs: 2-byte stores took 6 of the product's 15 us).
 template <typename T, int W>
-__device__ __forceinline__ void store_slab(const T* slab, T* out, int64_t N, int nrow, int ncol, bool wide, int lane) {
+__device__ __forceinline__ void store_slab(const T* slab, T* out, int64_t N, int nrow, int ncol, int lane) {
     constexpr int P = W + 16 / (int)sizeof(T), V = 16 / (int)sizeof(T), PER = W / V;
-    if (wide && ncol >= W) {
+    const int c = V * (lane % PER);
+    if (c + V <= ncol) {
 #pragma unroll 4
+        for (int r = lane / PER; r < nrow; r += 64 / PER) {
+            const u32x4 v = *(const u32x4*)&slab[r * P + c];
+            __builtin_memcpy(out + r * N + c, &v, 16);
+        }
+    } else if (c < ncol) {
         for (int r = lane / PER; r < nrow; r += 64 / PER)
-            *(u32x4*)(out + r * N + V * (lane % PER)) = *(const u32x4*)&slab[r * P + V * (lane % PER)];
-    } else {
-        for (int r = 0; r < nrow; ++r)
-            for (int c = lane; c < W && c < ncol; c += 64) out[r * N + c] = slab[r * P + c];
+            for (int k = c; k < ncol; ++k) out[r * N + k] = slab[r * P + k];
     }
 }
 
@@ -415,7 +420,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_gemm(TileArgs p) {
                             f32x4{value(j, 4 * g), value(j, 4 * g + 1), value(j, 4 * g + 2), value(j, 4 * g + 3)};
                 __builtin_amdgcn_wave_barrier();
                 store_slab<float, W>(fs, (float*)p.out + eout + row0 * p.N + c0 + 32 * j0, p.N, nrow, ncol - 32 * j0,
-                                     p.N % 4 == 0 && ((uintptr_t)p.out & 15) == 0, 32 * half + lr);
+                                     32 * half + lr);
                 __builtin_amdgcn_wave_barrier();
             }
         } else {
@@ -428,7 +433,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_gemm(TileArgs p) {
                         u32x2{pack16(p.type, value(j, 4 * g), value(j, 4 * g + 1)), pack16(p.type, value(j, 4 * g + 2), value(j, 4 * g + 3))};
             __builtin_amdgcn_wave_barrier();
             store_slab<uint16_t, WC>(hs, (uint16_t*)p.out + eout + row0 * p.N + c0, p.N, nrow, ncol,
-                                     p.N % 8 == 0 && ((uintptr_t)p.out & 15) == 0, 32 * half + lr);
+                                     32 * half + lr);
             __builtin_amdgcn_wave_barrier();
         }
     }
@@ -647,9 +652,10 @@ __global__ __launch_bounds__(64 * W) void k_mx_skinny(SkinnyArgs p) {
             for (int c = 0; c < 4; ++c) v[c] = zero ? 0.0f : v[c] * f;
         }
         const int64_t at = (m0 + r) * t.N + n;
-        if (n + 4 <= t.N && t.N % 4 == 0 && ((uintptr_t)t.out & 15) == 0) {
-            if (t.type == MX_F32) *(f32x4*)((float*)t.out + at) = v;
-            else *(u32x2*)((uint16_t*)t.out + at) = u32x2{pack16(t.type, v[0], v[1]), pack16(t.type, v[2], v[3])};
+        if (n + 4 <= t.N) {
+            const u32x2 h = {pack16(t.type, v[0], v[1]), pack16(t.type, v[2], v[3])};
+            if (t.type == MX_F32) __builtin_memcpy((float*)t.out + at, &v, 16);
+            else __builtin_memcpy((uint16_t*)t.out + at, &h, 8);
         } else {
             for (int c = 0; c < 4 && n + c < t.N; ++c) {
                 if (t.type == MX_F32) ((float*)t.out)[at + c] = v[c];
