@@ -374,6 +374,24 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_gemm(TileArgs p) {
 
     // The next tile's first stage is brought while this one's outputs leave.
     const int64_t em0 = m0, en0 = n0, eend = mend, eout = out0;
+    half = hidden(lane) >> 5;
+    lr = hidden(lane) & 31;
+    // the rows' factors, loaded ahead of it (loads come back in order)
+    float factor[FM];
+    bool zero[FM];
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+        const int64_t row = em0 + wm * (BM / WM) + 32 * i + lr;
+        factor[i] = 1.0f;
+        zero[i] = false;
+        if constexpr (GROUPED) {
+            if (row < eend) {
+                if (p.row_scale) factor[i] = p.row_scale[row];
+                // a row index outside a stands for a row of zeros
+                if (p.rows && (uint32_t)p.rows[row] >= (uint64_t)p.A) zero[i] = true;
+            }
+        }
+    }
     tile += stride;
     const bool more = tile < tile_end;
     if (more) {
@@ -388,25 +406,14 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_gemm(TileArgs p) {
     // 8 (a / 4) + 4 (l / 32) + a % 4 of operand b (a column), of a 32 x 32 block.
     // A wave turns 32 rows at a time around in LDS of its own and stores whole
     // runs of a row.
-    half = hidden(lane) >> 5;
-    lr = hidden(lane) & 31;
     constexpr int WC = BN / WN;
     const int64_t c0 = en0 + wn * WC;
     const int ncol = (int)(p.N - c0 < WC ? p.N - c0 : WC);
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
-        const int64_t row0 = em0 + wm * (BM / WM) + 32 * i, row = row0 + lr;
+        const int64_t row0 = em0 + wm * (BM / WM) + 32 * i;
         const int nrow = (int)(eend - row0 < 32 ? eend - row0 : 32);
-        float f = 1.0f;
-        bool zero = false;
-        if constexpr (GROUPED) {
-            if (row < eend) {
-                if (p.row_scale) f = p.row_scale[row];
-                // a row index outside a stands for a row of zeros
-                if (p.rows && (uint32_t)p.rows[row] >= (uint64_t)p.A) zero = true;
-            }
-        }
-        auto value = [&](int j, int a) { return zero ? 0.0f : acc[i][j][a] * f; };
+        auto value = [&](int j, int a) { return zero[i] ? 0.0f : acc[i][j][a] * factor[i]; };
         if (p.type == MX_F32) {
             constexpr int W = FN == 1 ? 32 : 64;
             float* const fs = (float*)slab;
