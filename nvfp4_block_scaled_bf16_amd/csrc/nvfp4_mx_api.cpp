@@ -86,7 +86,8 @@ nvfp4_status cast_impl(const void* x, int type, int64_t M, int64_t K, int64_t ld
     if (!row_q && !col_q) return fail(NVFP4_EINVAL, "no output direction requested");
     const int64_t tiles = offsets ? mx_max_tiles(R, E, 128) : up(R, 128) / 128;
     if ((s = check_grid(2 * tiles + 2, up(K, 128) / 128, "cast")) != NVFP4_OK) return s;
-    if (R == 0 || K == 0 || (rows == nullptr && M == 0)) return ok();
+    if (R == 0 || K == 0) return ok();
+    if (M == 0) return fail(NVFP4_EINVAL, "rows of an empty x (M=0, R=%lld)", (long long)R);
     const MxCast c{x, type, M, K, ldx, rows, R, offsets, E, row_q, row_sf, col_q, col_sf};
     return (s = check_hip(launch_mx_cast(c, as_stream(stream)), "mx cast")) != NVFP4_OK ? s : ok();
 }
@@ -173,7 +174,7 @@ nvfp4_status nvfp4_mx_wgrad_grouped(const uint8_t* a_q, const uint8_t* a_sf, con
     nvfp4_status s;
     if ((s = check_groups(offsets, num_groups, nullptr, nullptr)) != NVFP4_OK ||
         (s = check_type(out_type, "output")) != NVFP4_OK || (s = check_count(N, kMaxRows, "N")) != NVFP4_OK ||
-        (s = check_count(K, kMaxRows, "K")) != NVFP4_OK || (s = check_count(Tp, 2 * kMaxRows, "Tp")) != NVFP4_OK)
+        (s = check_count(K, kMaxRows, "K")) != NVFP4_OK || (s = check_count(Tp, kMaxK, "Tp")) != NVFP4_OK)
         return s;
     if (Tp % 128 != 0) return fail(NVFP4_ESHAPE, "Tp must be a multiple of 128 (Tp=%lld)", (long long)Tp);
     if (N == 0 || K == 0 || num_groups == 0) return ok();

@@ -650,9 +650,9 @@ __global__ __launch_bounds__(64 * W) void k_mx_skinny(SkinnyArgs p) {
         const int l = o & 63, tile = o >> 6, r = 16 * (tile % MT) + (l & 15);
         const int64_t n = n0 + 16 * (tile / MT) + 4 * (l >> 4);
         if (r >= nrow || n >= t.N) continue;
-        if (GROUPED && t.row_scale) {
-            const float f = t.row_scale[m0 + r];
-            // an outside row stays zero under an infinite factor
+        if constexpr (GROUPED) {
+            const float f = t.row_scale ? t.row_scale[m0 + r] : 1.0f;
+            // an outside row is zero whatever its factor or the weights
             const int64_t src = source(r);
             const bool zero = src < 0 || src >= t.A;
 #pragma unroll

@@ -161,6 +161,12 @@ def test_an_outside_row_is_zero_beside_a_nan():
         off = torch.tensor([0, n // 2, n], dtype=torch.int32, device="cuda")
         got = nv.mx_linear_grouped(x, bq, bsf, off, rows=idx[:n]).float()
         assert (got[0::2] == 0).all() and torch.isfinite(got).all()
+        # nor a factor's or a weight's
+        f = torch.full((n,), float("inf"), device="cuda")
+        wsf = bsf.clone()
+        wsf[:, 0, 0, :] = 255
+        got = nv.mx_linear_grouped(x, bq, wsf, off, rows=idx[:n], row_scale=f).float()
+        assert (got[0::2] == 0).all() and torch.isnan(got[1::2]).all()
 
 
 @pytest.mark.parametrize("R", [30, 400])

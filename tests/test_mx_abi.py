@@ -44,6 +44,7 @@ def test_quantize_grouped():
     assert q(F, BF16, 16, 16, 16, F, BIG, F, 2, F, F, F, F, None) == ESHAPE
     assert q(F, BF16, 16, 16, 16, F + 2, 17, F, 2, F, F, F, F, None) == EALIGN
     assert q(F, BF16, 16, 16, 16, None, 16, F + 1, 2, F, F, F, F, None) == EALIGN
+    assert q(None, BF16, 0, 16, 16, F, 5, F, 2, F, F, F, F, None) == EINVAL        # rows of nothing
 
 
 def test_dequantize():
@@ -83,6 +84,7 @@ def test_grouped_and_wgrad():
     assert g(*a(N=0)) == OK and g(*a(E=0)) == OK and g(*a(A=0, R=0)) == OK
     w = L().nvfp4_mx_wgrad_grouped
     assert w(F, F, F, F, 4, 4, 100, F, 2, 0, F, None) == ESHAPE
+    assert w(F, F, F, F, 4, 4, (1 << 23) + 128, F, 2, 0, F, None) == ESHAPE
     assert w(F, F, F, F, 4, 4, 128, None, 2, 0, F, None) == EINVAL
     assert w(F, F, F, F, 4, -4, 128, F, 2, 0, F, None) == EINVAL
     assert w(F, F, F, F, BIG - 1, 256, 128, F, 1 << 20, 0, F, None) == ESHAPE
