@@ -127,7 +127,7 @@ __device__ __forceinline__ void store_slab(const T* slab, T* out, int64_t N, int
 }
 
 template <int BM, int BN, int WM, int WN, int ST, int MODE>
-__global__ __launch_bounds__(64 * WM * WN) void k_mx_gemm(TileArgs p) {
+__global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2))) void k_mx_gemm(TileArgs p) {
     constexpr int NT = 64 * WM * WN, FM = BM / WM / 32, FN = BN / WN / 32;
     constexpr bool GROUPED = MODE == GEMM_GROUPED || MODE == GEMM_GROUPED_FAR;
     // loads a thread issues per stage: of a's codes, b's and the scales
@@ -327,6 +327,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_gemm(TileArgs p) {
 #pragma unroll
             for (int n = 0; n < (u + 1 < ST ? L : L1); ++n) bring(n, clamped(u), S[u]);
         asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"((ST - 2) * L + L1) : "memory");
+        if (m0 + wm * (BM / WM) < mend && n0 + wn * (BN / WN) < p.N) {
 #pragma unroll
         for (int z = 0; z < FM + FN; ++z) {
             read(S[0], 0, z, f0);
@@ -367,6 +368,17 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_gemm(TileArgs p) {
             quarter(Q2{}, f0, sc, f1, cur, 3, nullptr, L, L, 0, cur);
             drop(f1);
             quarter(Q3{}, f1, sc, f0, cur, -1, nullptr, L, L, 0, cur);
+        }
+        } else {
+            // a wave whose part of the tile lies outside brings its share of the loads alone
+            for (int64_t s = 0; s < nfull; ++s) {
+                GemmStage<BM, BN>&last = S[(s + ST - 1) % ST], &cur = S[s % ST];
+#pragma unroll
+                for (int n = L1; n < L; ++n) bring(n, clamped(s + ST - 1), last);
+                asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"((ST - 2) * L) : "memory");
+#pragma unroll
+                for (int n = 0; n < L1; ++n) bring(n, clamped(s + ST), cur);
+            }
         }
         // no load is on its way to LDS any more, and every wave is done with it
         asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
