@@ -760,16 +760,27 @@ constexpr int64_t kFewOutputs = int64_t(1) << 19;
 
 }  // namespace
 
-// Rows up to which the product casts x itself instead of in a launch before it.
-// Each workgroup casts its own: 1 x 8192 -> 28672 26 us with or without, 8 rows
-// 38 us against 28 and a cast of 3; 32 rows over 64 experts of 4096 x 4096 33 us
-// against 33 and a cast of 3, 64 rows 71 against 66.
-constexpr int64_t kCastDense = 4, kCastGrouped = 32;
-constexpr int kCastUnit = 8;    // rows to a grouped workgroup
+// Whether the product casts x itself instead of in a launch before it.  Each
+// workgroup casts its own rows, so that costs time with rows x workgroups x K;
+// the launch it saves costs the GPU 4 us and the host 3.5.  A call, with and
+// without: 16 x 4096 -> 4096 (2^24 elements cast) 8.5 us and 10.5, 8 x 8192 ->
+// 8192 (2^25) 13.5 and 10.7; 256 rows of 1024 over 16 experts of 2048 (2^24)
+// 12.5 and 13.0, 903 rows of 1000 over 33 of 777 (23 million) 19.9 and 12.2.
+constexpr int64_t kCastWork = int64_t(1) << 24;
+constexpr int kCastRows = 16;             // rows to a workgroup at most
+constexpr int64_t kCastGroupedRows = 1024;
 
-bool mx_linear_casts(int64_t M, int64_t Kp) { return M <= kCastDense && cast_rows(Kp / kMxStep) >= M; }
+// columns to a workgroup: 16, or 32 where several rows go to many workgroups
+int cast_columns(int64_t M, int64_t N, bool grouped) { return grouped || (M > 1 && N > 16 * 1024) ? 32 : 16; }
 
-bool mx_linear_grouped_casts(int64_t R, int64_t Kp) { return R <= kCastGrouped && cast_rows(Kp / kMxStep) >= kCastUnit; }
+bool mx_linear_casts(int64_t M, int64_t N, int64_t Kp) {
+    const int most = cast_rows(Kp / kMxStep), cols = cast_columns(M, N, false);
+    return M <= (most < kCastRows ? most : kCastRows) && M * ((N + cols - 1) / cols) <= kCastWork / (Kp > 0 ? Kp : 1);
+}
+
+bool mx_linear_grouped_casts(int64_t R, int64_t N, int64_t Kp) {
+    return R <= kCastGroupedRows && cast_rows(Kp / kMxStep) >= 8 && R * ((N + 31) / 32) <= kCastWork / (Kp > 0 ? Kp : 1);
+}
 
 hipError_t launch_mx_gemm(const MxGemm& g, hipStream_t st) {
     if (g.M <= 0 || g.N <= 0) return hipSuccess;
@@ -792,6 +803,7 @@ hipError_t launch_mx_gemm(const MxGemm& g, hipStream_t st) {
 template <int IN>
 hipError_t launch_casting(const SkinnyArgs& s, hipStream_t st) {
     if (s.t.offsets) return launch_skinny<1, 2, 4, IN, true>(s, mx_max_tiles(s.t.M, s.t.E, s.unit), st);
+    if (cast_columns(s.t.M, s.t.N, false) == 32) return launch_skinny<1, 2, 4, IN, false>(s, 1, st);
     return launch_skinny<1, 1, 4, IN, false>(s, 1, st);
 }
 
@@ -799,7 +811,8 @@ hipError_t launch_mx_linear(const MxGemm& g, const MxCast& c, hipStream_t st) {
     if (g.M <= 0 || g.N <= 0) return hipSuccess;
     TileArgs p{nullptr, nullptr, g.b_q, g.b_sf, g.A, g.M, g.N, g.Kp / kMxStep, g.out, g.type, g.offsets, g.E, g.M,
                g.rows, g.row_scale, 0, 0};
-    const SkinnyArgs s{p, c.x, c.K, c.ldx, g.offsets ? kCastUnit : (int)g.M};
+    // groups in tiles of 8 rows, which few rows to a group mostly fill no better
+    const SkinnyArgs s{p, c.x, c.K, c.ldx, g.offsets ? 8 : (int)g.M};
     if (c.type == MX_F32) return launch_casting<MX_F32>(s, st);
     if (c.type == MX_BF16) return launch_casting<MX_BF16>(s, st);
     return launch_casting<MX_F16>(s, st);

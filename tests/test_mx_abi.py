@@ -104,12 +104,12 @@ def test_linear_needs_its_workspace():
     assert f(F, BF16, 500, 300, 300, F, None, 256, BF16, F, F, n, None) == EINVAL
     assert f(F, BF16, 500, -3, 300, F, F, 256, BF16, F, F, n, None) == EINVAL
     h, need = L().nvfp4_mx_linear_grouped, L().nvfp4_mx_linear_grouped_workspace
-    n = need(500, 700, 256, 300)
+    n = need(500, 700, 4096, 300)
     assert n > 0
-    assert h(F, BF16, 500, 300, 300, F, 700, F, 4, F, F, 256, None, BF16, F, F, n - 1, None) == EINVAL
-    assert h(F, BF16, 500, 300, 300, None, 700, F, 4, F, F, 256, None, BF16, F, F, n, None) == EINVAL
-    assert h(F, BF16, 0, 300, 300, F, 700, F, 4, F, F, 256, None, BF16, F, F, n, None) == EINVAL
-    assert h(F, BF16, 500, 300, 300, F, 700, None, 4, F, F, 256, None, BF16, F, F, n, None) == EINVAL
+    assert h(F, BF16, 500, 300, 300, F, 700, F, 4, F, F, 4096, None, BF16, F, F, n - 1, None) == EINVAL
+    assert h(F, BF16, 500, 300, 300, None, 700, F, 4, F, F, 4096, None, BF16, F, F, n, None) == EINVAL
+    assert h(F, BF16, 0, 300, 300, F, 700, F, 4, F, F, 4096, None, BF16, F, F, n, None) == EINVAL
+    assert h(F, BF16, 500, 300, 300, F, 700, None, 4, F, F, 4096, None, BF16, F, F, n, None) == EINVAL
 
 
 def test_status_reaches_python():
