@@ -43,8 +43,10 @@ __device__ __forceinline__ uint32_t pack16(int type, float a, float b) {
 // blocks 0 .. 3 of the stage and lanes 32-63 blocks 4 .. 7, one of each to a
 // quarter, so that a lane's scales for the whole stage are one word.
 //
-// LDS: row r's eight 16-byte chunks at 128 r, chunk c in place c ^ (r % 8): 8
-// lanes reading one chunk of 8 rows touch every bank once.
+// LDS: row r's eight 16-byte chunks at 128 r, chunk c in place c ^ (r / 2 % 8):
+// the 16 lanes that one cycle serves read one chunk of 16 rows, 256 bytes that
+// touch each of the 64 banks once (with r % 8 rows r and r + 8 met: 47 % of the
+// LDS cycles were conflicts).
 //
 // What bounds it is power: random codes hold the chip near 1.45 GHz (the
 // matrix cores alone, without any load, run at 1.6 GHz and reach 6.4 PFLOP/s),
@@ -60,6 +62,8 @@ __device__ __forceinline__ uint32_t pack16(int type, float a, float b) {
 // (two more vector additions a load: 32768 rows of 4096 over 64 experts took 8 %
 // longer)
 enum GemmMode { GEMM_DENSE, GEMM_GROUPED, GEMM_GROUPED_FAR, GEMM_WGRAD };
+
+__device__ __forceinline__ int chunk_place(int c, int row) { return c ^ ((row >> 1) & 7); }
 
 template <int BM, int BN>
 struct GemmStage {
@@ -175,7 +179,7 @@ __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2)
     uint32_t qb[QB];
     int second[SL], sdst[SL];
     auto setup = [&](uint32_t id) __attribute__((always_inline)) {
-        const int t = hidden(tid), qc = (t & 7) ^ ((t >> 3) & 7);
+        const int t = hidden(tid), qc = chunk_place(t & 7, t >> 3);
         uint32_t tm, tn;
         int64_t step0 = 0;
         const uint8_t *b_q = p.b_q, *b_sf = p.b_sf;
@@ -238,7 +242,7 @@ __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2)
     };
     // load n of L of stage k; an odd last step's stage takes it twice, the second
     // time as zeros
-    const uint32_t back = (uint32_t)((tid ^ (tid >> 3)) & 4) * 16;
+    const uint32_t back = (uint32_t)(chunk_place(tid & 7, tid >> 3) & 4) * 16;
     auto bring = [&](int n, int64_t k, GemmStage<BM, BN>& st) __attribute__((always_inline)) {
         const bool cut = 2 * k + 1 >= steps;
         const uint32_t bb = cut ? back : 0u;
@@ -280,7 +284,7 @@ __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2)
         struct Scales { int v[FM + FN]; };
         auto tile_row = [&](int z) { return z < FN ? BM + wn * (BN / WN) + 32 * z + lr : wm * (BM / WM) + 32 * (z - FN) + lr; };
         auto read = [&](const GemmStage<BM, BN>& st, int quarter, int z, Frags& f) __attribute__((always_inline)) {
-            f.v[z] = *(const u32x4*)&st.q[tile_row(z) * 128 + 16 * ((4 * half + quarter) ^ (lr & 7))];
+            f.v[z] = *(const u32x4*)&st.q[tile_row(z) * 128 + 16 * chunk_place(4 * half + quarter, lr)];
         };
         auto read_scale = [&](const GemmStage<BM, BN>& st, int z, Scales& f) __attribute__((always_inline)) {
             f.v[z] = (int)st.sf[half][tile_row(z)];
