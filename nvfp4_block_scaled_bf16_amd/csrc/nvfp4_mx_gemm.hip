@@ -48,15 +48,20 @@ __device__ __forceinline__ uint32_t pack16(int type, float a, float b) {
 // touch each of the 64 banks once (with r % 8 rows r and r + 8 met: 47 % of the
 // LDS cycles were conflicts).
 //
-// What bounds it is power: random codes hold the chip near 1.45 GHz (the
-// matrix cores alone, without any load, run at 1.6 GHz and reach 6.4 PFLOP/s),
-// and the loop takes 1325 cycles per 128 elements where the matrix cores need
-// 1024.  16384 x 8192 x 8192: 575 us = 3.8 PFLOP/s.  Steps that led here, same
-// size: 128 x 128 tiles, 128-element stages, all of a stage's reads and loads
-// before its MFMAs 863 us; 256 x 256 tiles 730; outputs turned around in LDS
-// instead of 2-byte stores, tiles in XCD order 691; whole cache lines and each
-// LDS read and load placed between MFMAs 575 (the reads alone held up the
-// MFMAs for 400 cycles a step, the loads, half a line each, for another 400).
+// A workgroup takes several tiles: the next one's first stage is on its way
+// while this one's outputs leave.
+//
+// What bounds it is power: 16384 x 8192 x 8192 takes 509-524 us (4.2-4.3
+// PFLOP/s) at 1.67 GHz with the matrix cores busy in 62 % of the cycles; alone,
+// on registers of random codes and without any load, they hold the chip to 1.6
+// GHz and reach 6.4. A 256 x 256 tile's loop takes 1270 cycles per 128 elements
+// where the matrix cores need 1024, and 10 600 cycles lie between two tiles'
+// loops. Steps that led here, same size: 128 x 128 tiles, 128-element stages,
+// all of a stage's reads and loads before its MFMAs 863 us; 256 x 256 tiles 730;
+// outputs turned around in LDS instead of 2-byte stores, tiles in XCD order 691;
+// whole cache lines and each LDS read and load placed between MFMAs 575 (the
+// reads alone held up the MFMAs for 400 cycles a step, the loads, half a line
+// each, for another 400); several tiles to a workgroup 509.
 
 // GEMM_GROUPED_FAR: an operand a of 4 GB or more, whose rows need 64-bit offsets
 // (two more vector additions a load: 32768 rows of 4096 over 64 experts took 8 %
@@ -484,7 +489,7 @@ hipError_t launch_tiles(TileArgs p, int64_t mtiles, int64_t batch, hipStream_t s
 
 // ------------------------------------------------------------- few rows
 //
-// Bound by the weights' bytes (17 bits per 32 elements).  A workgroup takes 16
+// Bound by the weights' bytes (17 per 32 elements).  A workgroup takes 16
 // NT vectors of b and up to 16 MT rows of a; its waves split the sum, each
 // streaming its part of b from memory straight into the registers of
 // v_mfma_scale 16x16x128 (lane l: vector l % 16, block l / 16 of the step),
@@ -492,6 +497,12 @@ hipError_t launch_tiles(TileArgs p, int64_t mtiles, int64_t batch, hipStream_t s
 //
 // IN >= 0: a is x itself, of that type: the workgroup casts its rows into LDS
 // while its first loads of b are on their way, instead of a launch before it.
+//
+// 1 x 8192 -> 28672: 21-26 us, 4.8-5.9 TB/s of weights where a plain read of
+// as many bytes reaches 6.1.  A wave's steps in one run instead of in turn with
+// the other waves' 30 -> 26 us; 4 or 8 steps ahead and 8 or 16 waves change
+// nothing or cost registers.  More rows read all of a for every 16 NT columns:
+// 8192 -> 8192 takes 8 us for one row, 11, 13 and 15 for 32, 48 and 64.
 
 constexpr int kDeep = 2;
 
