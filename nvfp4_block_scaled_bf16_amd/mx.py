@@ -16,6 +16,8 @@ One linear layer, forward and backward::
 """
 from __future__ import annotations
 
+import functools
+
 import torch
 
 from . import _check, lib
@@ -29,8 +31,15 @@ _U8 = torch.uint8
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _stream(index):
-    return _raw_stream(index) if _raw_stream else torch.cuda.current_stream(index).cuda_stream
+def _call(index, fn, *args):
+    """fn on the current stream of device `index`, which is made the current
+    device for it where it is not (the default stream's handle names none)."""
+    if index != torch.cuda.current_device():
+        with torch.cuda.device(index):
+            return _call(index, fn, *args)
+    st = fn(*args, _raw_stream(index) if _raw_stream else torch.cuda.current_stream(index).cuda_stream)
+    if st:
+        _check(st)
 
 
 def _up(n, m):
@@ -81,12 +90,17 @@ def _codes(q, sf, name, batch=False):
     length and device."""
     if not isinstance(q, torch.Tensor) or q.dim() != 2 + batch or q.shape[-1] % 64:
         raise ValueError(f"{name}_q must be a {2 + batch}-D uint8 CUDA tensor with rows of a multiple of 64 bytes")
-    index = q.get_device()
-    qp = _tensor(q, _U8, index, f"{name}_q")
-    shape = q.shape
-    rows, Kp = shape[-2], 2 * shape[-1]
-    want = mx_sf_shape(rows, Kp)
-    return qp, _tensor(sf, _U8, index, f"{name}_sf", (shape[0],) + want if batch else want), rows, Kp, index
+    shape, index = q.shape, q.get_device()
+    rows, half = shape[-2], shape[-1]
+    want = (-(-rows // 128), half // 64, 128, 4)
+    if batch:
+        want = (shape[0],) + want
+    # the checks of _tensor on both at once; it names what is wrong
+    if not (q.dtype is _U8 and q.is_contiguous() and index >= 0 and isinstance(sf, torch.Tensor) and sf.dtype is _U8
+            and sf.is_contiguous() and sf.get_device() == index and sf.shape == want):
+        _tensor(q, _U8, index, f"{name}_q")
+        _tensor(sf, _U8, index, f"{name}_sf", want)
+    return q.data_ptr(), sf.data_ptr(), rows, 2 * half, index
 
 
 def _groups(offsets, rows, R, index):
@@ -130,9 +144,7 @@ def mx_quantize(x: torch.Tensor, rowwise: bool = True, columnwise: bool = True) 
     t, M, K, ldx = _matrix(x)
     out, p = _outputs(x, rowwise, columnwise, M, K, M)
     if M and K:
-        st = lib().nvfp4_mx_quantize(x.data_ptr(), t, M, K, ldx, *p, _stream(x.get_device()))
-        if st:
-            _check(st)
+        _call(x.get_device(), lib().nvfp4_mx_quantize, x.data_ptr(), t, M, K, ldx, *p)
     return out
 
 
@@ -147,9 +159,7 @@ def mx_quantize_grouped(x: torch.Tensor, offsets: torch.Tensor, rows: torch.Tens
     op, rp, E, R = _groups(offsets, rows, M, index)
     out, p = _outputs(x, rowwise, columnwise, R, K, mx_padded_rows(R, E))
     if R and K and (rowwise or E):
-        st = lib().nvfp4_mx_quantize_grouped(x.data_ptr(), t, M, K, ldx, rp, R, op, E, *p, _stream(index))
-        if st:
-            _check(st)
+        _call(index, lib().nvfp4_mx_quantize_grouped, x.data_ptr(), t, M, K, ldx, rp, R, op, E, *p)
     return out
 
 
@@ -160,9 +170,7 @@ def mx_dequantize(q: torch.Tensor, sf: torch.Tensor, K: int, out_dtype=torch.flo
     if not 0 <= K <= Kp or Kp != _up(K, 128):
         raise ValueError(f"K={K} does not fit rows of {Kp} codes")
     out = q.new_empty((R, K), dtype=out_dtype)
-    st = lib().nvfp4_mx_dequantize(qp, sp, R, K, t, out.data_ptr(), _stream(index))
-    if st:
-        _check(st)
+    _call(index, lib().nvfp4_mx_dequantize, qp, sp, R, K, t, out.data_ptr())
     return out
 
 
@@ -174,9 +182,7 @@ def mx_gemm(a_q, a_sf, b_q, b_sf, out_dtype=torch.bfloat16) -> torch.Tensor:
         raise ValueError("a and b differ in length or device")
     t = _type(out_dtype, "out_dtype")
     out = a_q.new_empty((M, N), dtype=out_dtype)
-    st = lib().nvfp4_mx_gemm(ap, asp, bp, bsp, M, N, K, t, out.data_ptr(), _stream(index))
-    if st:
-        _check(st)
+    _call(index, lib().nvfp4_mx_gemm, ap, asp, bp, bsp, M, N, K, t, out.data_ptr())
     return out
 
 
@@ -199,9 +205,7 @@ def mx_gemm_grouped(a_q, a_sf, b_q, b_sf, offsets, rows=None, row_scale=None,
     op, rp, E, R, fp = _grouped_shapes(offsets, rows, row_scale, A, b_q.shape[0], index, "b")
     t = _type(out_dtype, "out_dtype")
     out = a_q.new_empty((R, N), dtype=out_dtype)
-    st = lib().nvfp4_mx_gemm_grouped(ap, asp, A, rp, R, op, E, bp, bsp, N, K, fp, t, out.data_ptr(), _stream(index))
-    if st:
-        _check(st)
+    _call(index, lib().nvfp4_mx_gemm_grouped, ap, asp, A, rp, R, op, E, bp, bsp, N, K, fp, t, out.data_ptr())
     return out
 
 
@@ -216,9 +220,7 @@ def mx_wgrad_grouped(a_q, a_sf, b_q, b_sf, offsets, out_dtype=torch.float32) -> 
     op, _, E, _ = _groups(offsets, None, 0, index)
     t = _type(out_dtype, "out_dtype")
     out = a_q.new_empty((E, N, K), dtype=out_dtype)
-    st = lib().nvfp4_mx_wgrad_grouped(ap, asp, bp, bsp, N, K, Tp, op, E, t, out.data_ptr(), _stream(index))
-    if st:
-        _check(st)
+    _call(index, lib().nvfp4_mx_wgrad_grouped, ap, asp, bp, bsp, N, K, Tp, op, E, t, out.data_ptr())
     return out
 
 
@@ -231,9 +233,10 @@ def _weights(x, w_q, w_sf, out_dtype, batch):
     return xt, M, K, ldx, wp, wsp, N, index, out_dtype, _type(out_dtype, "out_dtype")
 
 
-def _workspace(x, n):
-    # freed to the stream's order as soon as the call has been enqueued
-    return x.new_empty(n, dtype=_U8) if n else None
+@functools.lru_cache(maxsize=1024)
+def _workspace_bytes(*sizes):
+    L = lib()
+    return (L.nvfp4_mx_linear_workspace if len(sizes) == 3 else L.nvfp4_mx_linear_grouped_workspace)(*sizes)
 
 
 def mx_linear(x: torch.Tensor, w_q, w_sf, out_dtype=None) -> torch.Tensor:
@@ -241,13 +244,11 @@ def mx_linear(x: torch.Tensor, w_q, w_sf, out_dtype=None) -> torch.Tensor:
     of x's type unless ``out_dtype`` is given."""
     xt, M, K, ldx, wp, wsp, N, index, out_dtype, t = _weights(x, w_q, w_sf, out_dtype, False)
     out = x.new_empty((M, N), dtype=out_dtype)
-    L = lib()
-    n = L.nvfp4_mx_linear_workspace(M, N, K)
-    ws = _workspace(x, n)
-    st = L.nvfp4_mx_linear(x.data_ptr(), xt, M, K, ldx, wp, wsp, N, t, out.data_ptr(),
-                           None if ws is None else ws.data_ptr(), n, _stream(index))
-    if st:
-        _check(st)
+    n = _workspace_bytes(M, N, K)
+    # freed in the stream's order once the call has been enqueued
+    ws = x.new_empty(n, dtype=_U8) if n else None
+    _call(index, lib().nvfp4_mx_linear, x.data_ptr(), xt, M, K, ldx, wp, wsp, N, t, out.data_ptr(),
+          ws.data_ptr() if n else None, n)
     return out
 
 
@@ -258,11 +259,8 @@ def mx_linear_grouped(x: torch.Tensor, w_q, w_sf, offsets, rows=None, row_scale=
     xt, M, K, ldx, wp, wsp, N, index, out_dtype, t = _weights(x, w_q, w_sf, out_dtype, True)
     op, rp, E, R, fp = _grouped_shapes(offsets, rows, row_scale, M, w_q.shape[0], index, "w")
     out = x.new_empty((R, N), dtype=out_dtype)
-    L = lib()
-    n = L.nvfp4_mx_linear_grouped_workspace(M, R, N, K)
-    ws = _workspace(x, n)
-    st = L.nvfp4_mx_linear_grouped(x.data_ptr(), xt, M, K, ldx, rp, R, op, E, wp, wsp, N, fp, t, out.data_ptr(),
-                                   None if ws is None else ws.data_ptr(), n, _stream(index))
-    if st:
-        _check(st)
+    n = _workspace_bytes(M, R, N, K)
+    ws = x.new_empty(n, dtype=_U8) if n else None
+    _call(index, lib().nvfp4_mx_linear_grouped, x.data_ptr(), xt, M, K, ldx, rp, R, op, E, wp, wsp, N, fp, t,
+          out.data_ptr(), ws.data_ptr() if n else None, n)
     return out

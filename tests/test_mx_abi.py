@@ -146,3 +146,28 @@ def test_padded_rows_cover_every_split():
             assert nv.mx_padded_rows(R, E) % 128 == 0
             assert most[E][R] <= nv.mx_padded_rows(R, E)
             assert R <= nv.mx_padded_rows(R, E)
+
+
+def test_another_device_is_made_current_for_the_call(monkeypatch):
+    import contextlib
+
+    from nvfp4_block_scaled_bf16_amd import mx
+
+    current, seen = [0], []
+
+    @contextlib.contextmanager
+    def device(index):
+        last, current[0] = current[0], index
+        yield
+        current[0] = last
+
+    def fn(*args):
+        seen.append((current[0], args))
+        return 0
+
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: current[0])
+    monkeypatch.setattr(torch.cuda, "device", device)
+    monkeypatch.setattr(mx, "_raw_stream", lambda index: 100 + index)
+    mx._call(0, fn, 7)
+    mx._call(1, fn, 8)
+    assert seen == [(0, (7, 100)), (1, (8, 101))] and current == [0]
