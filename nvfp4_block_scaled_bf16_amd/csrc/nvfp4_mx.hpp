@@ -31,6 +31,13 @@ constexpr int kMxStep = 128;                // elements of K per scale word
 // workgroups of one launch, in one grid dimension
 constexpr int64_t kMxMaxGrid = (int64_t(1) << 31) - 1;
 
+// Keeps one wave's LDS accesses before it apart from those after it: the
+// hardware does them in the order written, so only the compiler has to be told.
+__device__ __forceinline__ void lds_in_order() {
+    __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
 // byte offset of the scale word of vector r, 128-element step kt
 __device__ __forceinline__ int64_t mx_sf_offset(int64_t r, int64_t kt, int64_t Kt) {
     return (((r >> 7) * Kt + kt) * 128 + (r & 127)) * 4;

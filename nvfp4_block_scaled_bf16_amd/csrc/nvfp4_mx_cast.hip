@@ -244,7 +244,7 @@ __global__ __launch_bounds__(64 * W) void k_mx_tile(MxCast c, uint32_t nkt, int6
         const uint32_t k0 = scale_code16<T>(mm[0] & 0xffffu), k1 = scale_code16<T>(mm[0] >> 16);
         uint8_t* const mine = S.rsf[wave][lane >> 4];
         *(uint16_t*)&mine[2 * (lane & 15)] = (uint16_t)(k0 | k1 << 8);
-        __builtin_amdgcn_wave_barrier();
+        lds_in_order();
         uint32_t code[8];
         *(u32x4*)&code[0] = *(const u32x4*)&mine[0];
         *(u32x4*)&code[4] = *(const u32x4*)&mine[16];

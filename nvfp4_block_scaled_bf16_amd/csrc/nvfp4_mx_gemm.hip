@@ -446,10 +446,10 @@ __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2)
                     for (int g = 0; g < 4; ++g)
                         *(f32x4*)&fs[lr * (W + 4) + 32 * (j - j0) + 8 * g + 4 * half] =
                             f32x4{value(j, 4 * g), value(j, 4 * g + 1), value(j, 4 * g + 2), value(j, 4 * g + 3)};
-                __builtin_amdgcn_wave_barrier();
+                lds_in_order();
                 store_slab<float, W>(fs, (float*)p.out + eout + row0 * p.N + c0 + 32 * j0, p.N, nrow, ncol - 32 * j0,
                                      32 * half + lr);
-                __builtin_amdgcn_wave_barrier();
+                lds_in_order();
             }
         } else {
             uint16_t* const hs = (uint16_t*)slab;
@@ -459,10 +459,10 @@ __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2)
                 for (int g = 0; g < 4; ++g)
                     *(u32x2*)&hs[lr * (WC + 8) + 32 * j + 8 * g + 4 * half] =
                         u32x2{pack16(p.type, value(j, 4 * g), value(j, 4 * g + 1)), pack16(p.type, value(j, 4 * g + 2), value(j, 4 * g + 3))};
-            __builtin_amdgcn_wave_barrier();
+            lds_in_order();
             store_slab<uint16_t, WC>(hs, (uint16_t*)p.out + eout + row0 * p.N + c0, p.N, nrow, ncol,
                                      32 * half + lr);
-            __builtin_amdgcn_wave_barrier();
+            lds_in_order();
         }
     }
     if (!more) return;
@@ -491,20 +491,30 @@ hipError_t launch_tiles(TileArgs p, int64_t mtiles, int64_t batch, hipStream_t s
 //
 // Bound by the weights' bytes (17 per 32 elements).  A workgroup takes 16
 // NT vectors of b and up to 16 MT rows of a; its waves split the sum, each
-// streaming its part of b from memory straight into the registers of
-// v_mfma_scale 16x16x128 (lane l: vector l % 16, block l / 16 of the step),
-// kDeep steps ahead.  The waves' sums are added in LDS in their order.
+// streaming its part of b from memory, D pairs of steps ahead, into registers
+// and from there through LDS, which turns it around for v_mfma_scale 16x16x128
+// (lane l: vector l % 16, block l / 16 of the step).  The waves' sums are added
+// in LDS in their order.
+//
+// A load takes eight vectors' whole cache lines, eight lanes to a line.  Loaded
+// in the matrix core's order, neighbouring lanes belong to different vectors:
+// a load then takes one cycle a lane whatever the bytes, and those cycles, not
+// the memory, were the bound (rows x 8192 -> 28672, 16 and 64 rows: 33 and 58
+// us; half lines 32 and 49; whole lines 26 and 40).  The way through LDS costs
+// a write and a read in LDS of every byte, half of what it saves.
 //
 // IN >= 0: a is x itself, of that type: the workgroup casts its rows into LDS
 // while its first loads of b are on their way, instead of a launch before it.
+// Several rows take eight waves, which share the cast (8 x 8192 -> 8192 13.5
+// and 11.0 us with four and eight), one row four with two pairs ahead (1 x 8192
+// -> 28672 24.2 us; eight waves one pair ahead 25.6).
 //
-// 1 x 8192 -> 28672: 21-26 us, 4.8-5.9 TB/s of weights where a plain read of
+// 1 x 8192 -> 28672: 23 us a call, 5.4 TB/s of weights where a plain read of
 // as many bytes reaches 6.1.  A wave's steps in one run instead of in turn with
-// the other waves' 30 -> 26 us; 4 or 8 steps ahead and 8 or 16 waves change
-// nothing or cost registers.  More rows read all of a for every 16 NT columns:
-// 8192 -> 8192 takes 8 us for one row, 11, 13 and 15 for 32, 48 and 64.
-
-constexpr int kDeep = 2;
+// the other waves' saved an eighth.  More rows read all of a for every 16 NT
+// columns: 8192 -> 8192 takes 8 us for one row, 9.6, 10.6 and 12 for 32, 48 and
+// 64; twice the columns to a workgroup again gained 7 % at 16384 columns and
+// lost as much at 20480, where the workgroups then fill the chip unevenly.
 
 struct SkinnyArgs {
     TileArgs t;
@@ -513,7 +523,7 @@ struct SkinnyArgs {
     int unit;                   // rows of a to a workgroup, at most 16 MT
 };
 
-template <int MT, int NT, int W, int IN, bool GROUPED>
+template <int MT, int NT, int W, int D, int IN, bool GROUPED>
 __global__ __launch_bounds__(64 * W) void k_mx_skinny(SkinnyArgs p) {
     extern __shared__ __attribute__((aligned(16))) char lds[];
     const int tid = (int)threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -538,19 +548,24 @@ __global__ __launch_bounds__(64 * W) void k_mx_skinny(SkinnyArgs p) {
         return row;
     };
 
-    // this wave's steps: an even share of the pairs of steps, in one run
-    const int Kt = (int)t.Kt, pairs = (Kt + 1) / 2, first = pairs * wave / W * 2, last = pairs * (wave + 1) / W * 2;
-    const int cnt = (last < Kt ? last : Kt) - first;
+    // this wave's pairs of steps: an even share, in one run; an odd last step
+    // is alone in its pair
+    const int Kt = (int)t.Kt, pairs = (Kt + 1) / 2, first = pairs * wave / W, cnt = pairs * (wave + 1) / W - first;
+
+    // Load u of two of a tile's 16 vectors and a pair's 128 bytes: vector 8 u +
+    // line, chunk.  Scale words are loaded by lane l for vector l % 16.
+    const int line = lane >> 3, chunk = lane & 7;
 
     // vectors past the last repeat it, their sums are not stored
-    const uint8_t *bq[NT], *bs[NT];
+    const uint8_t *bq[NT][2], *bs[NT];
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
-        const int64_t n = n0 + 16 * j + lr < t.N ? n0 + 16 * j + lr : t.N - 1;
-        bq[j] = b_q + n * t.Kt * 64 + 16 * g;
-        bs[j] = b_sf + mx_sf_offset(n, 0, t.Kt);
+        auto clip = [&](int r) { return n0 + 16 * j + r < t.N ? n0 + 16 * j + r : t.N - 1; };
+#pragma unroll
+        for (int u = 0; u < 2; ++u) bq[j][u] = b_q + clip(8 * u + line) * t.Kt * 64 + 16 * chunk;
+        bs[j] = b_sf + mx_sf_offset(clip(lr), 0, t.Kt);
     }
-    const uint8_t *aq[MT], *as[MT];
+    const uint8_t *aq[MT][2], *as[MT];
     bool none[MT];                              // a row index outside a: a row of zeros
     if constexpr (IN < 0) {
 #pragma unroll
@@ -558,37 +573,49 @@ __global__ __launch_bounds__(64 * W) void k_mx_skinny(SkinnyArgs p) {
             int64_t row = source(16 * i + lr);
             none[i] = row < 0 || row >= t.A;
             row = none[i] ? 0 : row;
-            aq[i] = t.a_q + row * t.Kt * 64 + 16 * g;
             as[i] = t.a_sf + mx_sf_offset(row, 0, t.Kt);
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                row = source(16 * i + 8 * u + line);
+                aq[i][u] = t.a_q + (row < 0 || row >= t.A ? 0 : row) * t.Kt * 64 + 16 * chunk;
+            }
         }
     }
-    struct Step {
-        u32x4 b[NT], a[IN < 0 ? MT : 1];
-        uint32_t bs[NT], as[IN < 0 ? MT : 1];
+    struct Pair {
+        u32x4 b[NT][2], a[IN < 0 ? MT : 1][2];
+        uint32_t bs[NT][2], as[IN < 0 ? MT : 1][2];
     };
-    Step ring[kDeep];
-    auto load = [&](int i, Step& s) __attribute__((always_inline)) {
-        const int64_t k = first + (i < cnt ? i : cnt - 1);
+    Pair ring[D];
+    auto load = [&](int i, Pair& s) __attribute__((always_inline)) {
+        const int64_t k = 2 * (int64_t)(first + (i < cnt ? i : cnt - 1));
+        // a step alone is loaded twice
+        const bool alone = k + 1 >= Kt;
+        const int back = alone && chunk >= 4 ? 64 : 0, second = alone ? 0 : 512;
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-            s.b[j] = *(const u32x4*)(bq[j] + k * 64);
-            s.bs[j] = *(const uint32_t*)(bs[j] + k * 512);
-        }
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                s.b[j][u] = *(const u32x4*)(bq[j][u] + k * 64 - back);
+                s.bs[j][u] = *(const uint32_t*)(bs[j] + k * 512 + u * second);
+            }
         if constexpr (IN < 0) {
 #pragma unroll
-            for (int j = 0; j < MT; ++j) {
-                s.a[j] = *(const u32x4*)(aq[j] + k * 64);
-                s.as[j] = *(const uint32_t*)(as[j] + k * 512);
-            }
+            for (int j = 0; j < MT; ++j)
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    s.a[j][u] = *(const u32x4*)(aq[j][u] + k * 64 - back);
+                    s.as[j][u] = *(const uint32_t*)(as[j] + k * 512 + u * second);
+                }
         }
     };
     if (cnt > 0) {
 #pragma unroll
-        for (int d = 0; d < kDeep; ++d) load(d, ring[d]);
+        for (int d = 0; d < D; ++d) load(d, ring[d]);
     }
 
     const int pitch = Kt * 64 + 16;             // of a row's codes in LDS
     uint8_t* const lsf = (uint8_t*)lds + p.unit * pitch;
+    const int turn0 = IN >= 0 ? (p.unit * (Kt * 68 + 16) + 15) / 16 * 16 : 0;
     if constexpr (IN >= 0) {
         constexpr int B = IN == MX_F32 ? 4 : 2;
         const int per = Kt * 4;
@@ -621,45 +648,70 @@ __global__ __launch_bounds__(64 * W) void k_mx_skinny(SkinnyArgs p) {
 #pragma unroll
         for (int i = 0; i < MT; ++i) acc[j][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     const int row = lr < nrow ? lr : nrow - 1;
-    auto use = [&](int i, const Step& s) __attribute__((always_inline)) {
-        u32x4 a[MT];
-        int sa[MT];
+    // A pair on its way through this wave's LDS: vector v of a tile at 128 v, its
+    // chunk c in place c ^ (v / 2 % 8), so that neither side meets in a bank.  A
+    // wave's LDS accesses are done in the order written: nothing to wait for.
+    char* const turn = lds + turn0 + wave * ((NT + (IN < 0 ? MT : 0)) * 2048);
+    const int wat = 128 * line + 16 * chunk_place(chunk, line);   // chunk_place(c, r + 8) = chunk_place(c, r) ^ 4
+    auto use = [&](int i, Pair& s, bool more) __attribute__((always_inline)) {
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
-            if constexpr (IN >= 0) {
-                const int k = first + i;
-                a[m] = *(const u32x4*)(lds + row * pitch + k * 64 + 16 * g);
-                sa[m] = lsf[row * (Kt * 4) + 4 * k + g];
-            } else {
-                a[m] = none[m] ? u32x4{0, 0, 0, 0} : s.a[m];
-                sa[m] = none[m] ? 0 : (int)(s.as[m] >> (8 * g));
-            }
-        }
+        for (int j = 0; j < NT; ++j)
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-            const int sb = (int)(s.bs[j] >> (8 * g));
+            for (int u = 0; u < 2; ++u) *(u32x4*)(turn + 2048 * j + 1024 * u + (wat ^ (64 * u))) = s.b[j][u];
+        if constexpr (IN < 0) {
 #pragma unroll
             for (int m = 0; m < MT; ++m)
-                acc[j][m] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(frag(s.b[j]), frag(a[m]), acc[j][m], kFp4,
-                                                                             kFp4, 0, sb, 0, sa[m]);
+#pragma unroll
+                for (int u = 0; u < 2; ++u) *(u32x4*)(turn + 2048 * (NT + m) + 1024 * u + (wat ^ (64 * u))) = s.a[m][u];
         }
+        lds_in_order();
+        uint32_t bs[NT][2], as[IN < 0 ? MT : 1][2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+#pragma unroll
+            for (int j = 0; j < NT; ++j) bs[j][u] = s.bs[j][u];
+            if constexpr (IN < 0) {
+#pragma unroll
+                for (int m = 0; m < MT; ++m) as[m][u] = s.as[m][u];
+            }
+        }
+        if (more) load(i + D, s);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int k = 2 * (first + i) + u;
+            if (k >= Kt) break;
+            const int at = 128 * lr + 16 * chunk_place(4 * u + g, lr);
+            u32x4 a[MT], b[NT];
+            int sa[MT];
+#pragma unroll
+            for (int j = 0; j < NT; ++j) b[j] = *(const u32x4*)(turn + 2048 * j + at);
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                if constexpr (IN >= 0) {
+                    a[m] = *(const u32x4*)(lds + row * pitch + k * 64 + 16 * g);
+                    sa[m] = lsf[row * (Kt * 4) + 4 * k + g];
+                } else {
+                    a[m] = *(const u32x4*)(turn + 2048 * (NT + m) + at);
+                    a[m] = none[m] ? u32x4{0, 0, 0, 0} : a[m];
+                    sa[m] = none[m] ? 0 : (int)(as[m][u] >> (8 * g));
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                const int sb = (int)(bs[j][u] >> (8 * g));
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+                    acc[j][m] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(frag(b[j]), frag(a[m]), acc[j][m], kFp4,
+                                                                                 kFp4, 0, sb, 0, sa[m]);
+            }
+        }
+        lds_in_order();
     };
-    int i0 = 0;
-    for (; i0 + 2 * kDeep <= cnt; i0 += kDeep) {
+    for (int i0 = 0; i0 < cnt; i0 += D) {
 #pragma unroll
-        for (int d = 0; d < kDeep; ++d) {
-            use(i0 + d, ring[d]);
-            load(i0 + d + kDeep, ring[d]);
-        }
+        for (int d = 0; d < D; ++d)
+            if (i0 + d < cnt) use(i0 + d, ring[d], i0 + d + D < cnt);
     }
-#pragma unroll
-    for (int d = 0; d < kDeep; ++d) {
-        if (i0 + d < cnt) use(i0 + d, ring[d]);
-        if (i0 + d + kDeep < cnt) load(i0 + d + kDeep, ring[d]);
-    }
-#pragma unroll
-    for (int d = 0; d < kDeep; ++d)
-        if (i0 + d + kDeep < cnt) use(i0 + d + kDeep, ring[d]);
 
     // the waves' sums: [wave][tile][lane], then 4 consecutive columns of one
     // row to a thread
@@ -700,14 +752,15 @@ __global__ __launch_bounds__(64 * W) void k_mx_skinny(SkinnyArgs p) {
 }
 
 
-template <int MT, int NT, int W, int IN, bool GROUPED>
+template <int MT, int NT, int W, int D, int IN, bool GROUPED>
 hipError_t launch_skinny(SkinnyArgs p, int64_t mtiles, hipStream_t st) {
     const int64_t ntn = (p.t.N + 16 * NT - 1) / (16 * NT);
     if (mtiles > kMxMaxGrid || ntn > kMxMaxGrid || mtiles * ntn > kMxMaxGrid) return hipErrorInvalidValue;
     if (mtiles * ntn == 0) return hipSuccess;
     p.t.ntn = (uint32_t)ntn;
-    const int red = W * NT * MT * 1024, codes = IN >= 0 ? p.unit * (int)(p.t.Kt * 68 + 16) : 0;
-    k_mx_skinny<MT, NT, W, IN, GROUPED><<<(unsigned)(mtiles * ntn), 64 * W, red > codes ? red : codes, st>>>(p);
+    const int red = W * NT * MT * 1024, codes = IN >= 0 ? (p.unit * (int)(p.t.Kt * 68 + 16) + 15) / 16 * 16 : 0;
+    const int loop = codes + W * (NT + (IN < 0 ? MT : 0)) * 2048;
+    k_mx_skinny<MT, NT, W, D, IN, GROUPED><<<(unsigned)(mtiles * ntn), 64 * W, red > loop ? red : loop, st>>>(p);
     return hipGetLastError();
 }
 // ---------------------------------------------------------------- choices
@@ -750,8 +803,8 @@ hipError_t launch_best(const TileArgs& p, const int64_t* mtiles, int64_t batch, 
 template <int MT>
 hipError_t launch_few_nt(const SkinnyArgs& p, int64_t mtiles, hipStream_t st) {
     // twice the columns to a workgroup where that leaves one for every compute unit
-    if (mtiles * ((p.t.N + 31) / 32) >= kCus) return launch_skinny<MT, 2, 4, -1, false>(p, mtiles, st);
-    return launch_skinny<MT, 1, 4, -1, false>(p, mtiles, st);
+    if (mtiles * ((p.t.N + 31) / 32) >= kCus) return launch_skinny<MT, 2, 4, 2, -1, false>(p, mtiles, st);
+    return launch_skinny<MT, 1, 4, 2, -1, false>(p, mtiles, st);
 }
 
 hipError_t launch_few(const SkinnyArgs& p, int64_t rows, int64_t mtiles, hipStream_t st) {
@@ -762,7 +815,8 @@ hipError_t launch_few(const SkinnyArgs& p, int64_t rows, int64_t mtiles, hipStre
 }
 
 // Rows of x that a workgroup can hold as codes (0: too long a row): up to 16,
-// in at most 36 KB, so that four workgroups fit a compute unit.
+// in at most 36 KB, so that with the 32 KB on their way two workgroups fit a
+// compute unit.
 int cast_rows(int64_t Kt) {
     const int64_t n = 36 * 1024 / (Kt * 68 + 16);
     return (int)(n < 16 ? n : 16);
@@ -770,7 +824,7 @@ int cast_rows(int64_t Kt) {
 
 // The few-rows kernel reads all of a for every 16 or 32 columns, from the L2:
 // past this many outputs that costs more than what the tiles lose (8192 x
-// 8192: 64 rows 15 us against 16, 128 rows 27 against 16).
+// 8192: 64 rows 12 us against 13, 128 rows 16.5 against 13).
 constexpr int64_t kFewOutputs = int64_t(1) << 19;
 
 }  // namespace
@@ -785,11 +839,13 @@ constexpr int64_t kCastWork = int64_t(1) << 24;
 constexpr int kCastRows = 16;             // rows to a workgroup at most
 constexpr int64_t kCastGroupedRows = 1024;
 
-// columns to a workgroup: 16, or 32 where several rows go to many workgroups
-int cast_columns(int64_t M, int64_t N, bool grouped) { return grouped || (M > 1 && N > 16 * 1024) ? 32 : 16; }
+// columns to a workgroup: 16, or 32 where several rows' cast is repeated less
+// often by it and every compute unit still has a workgroup (8 x 8192 -> 8192
+// 12.1 and 11.0 us)
+int cast_columns(int64_t M, int64_t N) { return M > 1 && N > 32 * (kCus - 1) ? 32 : 16; }
 
 bool mx_linear_casts(int64_t M, int64_t N, int64_t Kp) {
-    const int most = cast_rows(Kp / kMxStep), cols = cast_columns(M, N, false);
+    const int most = cast_rows(Kp / kMxStep), cols = cast_columns(M, N);
     return M <= (most < kCastRows ? most : kCastRows) && M * ((N + cols - 1) / cols) <= kCastWork / (Kp > 0 ? Kp : 1);
 }
 
@@ -817,9 +873,18 @@ hipError_t launch_mx_gemm(const MxGemm& g, hipStream_t st) {
 
 template <int IN>
 hipError_t launch_casting(const SkinnyArgs& s, hipStream_t st) {
-    if (s.t.offsets) return launch_skinny<1, 2, 4, IN, true>(s, mx_max_tiles(s.t.M, s.t.E, s.unit), st);
-    if (cast_columns(s.t.M, s.t.N, false) == 32) return launch_skinny<1, 2, 4, IN, false>(s, 1, st);
-    return launch_skinny<1, 1, 4, IN, false>(s, 1, st);
+    if (s.t.offsets) {
+        // Two pairs ahead where a wave has more than two; fewer registers and
+        // more workgroups at once otherwise (one and two ahead: 32 rows of 4096
+        // over 64 experts of 4096 41.2 and 39.4 us a call, 256 rows of 1024 over
+        // 16 of 2048 12.4 and 14.0)
+        const int64_t mtiles = mx_max_tiles(s.t.M, s.t.E, s.unit);
+        if (s.t.Kt > 16) return launch_skinny<1, 2, 4, 2, IN, true>(s, mtiles, st);
+        return launch_skinny<1, 2, 4, 1, IN, true>(s, mtiles, st);
+    }
+    if (s.t.M == 1) return launch_skinny<1, 1, 4, 2, IN, false>(s, 1, st);
+    if (cast_columns(s.t.M, s.t.N) == 32) return launch_skinny<1, 2, 8, 1, IN, false>(s, 1, st);
+    return launch_skinny<1, 1, 8, 1, IN, false>(s, 1, st);
 }
 
 hipError_t launch_mx_linear(const MxGemm& g, const MxCast& c, hipStream_t st) {

@@ -42,6 +42,21 @@ def test_long_sums(M):
     mx_ref.check_product(nv.mx_gemm(aq, asf, bq, bsf, torch.float32), a, b)
 
 
+@pytest.mark.parametrize("M", [1, 2, 9, 33, 64])
+@pytest.mark.parametrize("K", [120, 200, 385, 1000, 1150, 2100])      # 1, 2, 4, 8, 9 and 17 steps
+def test_few_rows_by_steps(M, K):
+    # fewer steps than waves, an odd one left over, in both ways of few rows
+    rng = np.random.default_rng(M * 17 + K)
+    (aq, asf, a), (bq, bsf, b) = vectors(rng, M, K), vectors(rng, 77, K)
+    mx_ref.check_product(nv.mx_gemm(aq, asf, bq, bsf, torch.float32), a, b)
+    x = data(rng, M, K, torch.bfloat16)
+    fx = np.pad(mx_ref.fake(mx_ref.host64(x)), ((0, 0), (0, b.shape[1] - K)))
+    mx_ref.check_product(nv.mx_linear(x, bq, bsf, torch.float32), fx, b)
+    off = torch.tensor([0, M // 2, M], dtype=torch.int32, device="cuda")
+    w2, s2 = torch.stack([bq, bq]), torch.stack([bsf, bsf])
+    mx_ref.check_product(nv.mx_linear_grouped(x, w2, s2, off, out_dtype=torch.float32), fx, b)
+
+
 def test_large_tiles():
     # enough tiles for every tile shape, checked at whole rows
     rng = np.random.default_rng(3)
