@@ -285,10 +285,10 @@ struct MxGemm {
     const float* row_scale;      // optional: factor of row r
 };
 hipError_t launch_mx_gemm(const MxGemm& g, hipStream_t st);
-// whether launch_mx_linear takes this product (or the R grouped rows): x (c)
+// whether launch_mx_linear takes this product (or the R rows in E groups): x (c)
 // cast on the way, no operand a (g.a_q and g.a_sf unused)
 bool mx_linear_casts(int64_t M, int64_t N, int64_t Kp);
-bool mx_linear_grouped_casts(int64_t R, int64_t N, int64_t Kp);
+bool mx_linear_grouped_casts(int64_t R, int64_t E, int64_t N, int64_t Kp);
 hipError_t launch_mx_linear(const MxGemm& g, const MxCast& c, hipStream_t st);
 
 struct MxWgrad {

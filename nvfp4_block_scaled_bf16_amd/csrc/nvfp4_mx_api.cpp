@@ -224,7 +224,8 @@ nvfp4_status nvfp4_mx_linear(const void* x, nvfp4_dtype x_type, int64_t M, int64
 
 int64_t nvfp4_mx_linear_grouped_workspace(int64_t M, int64_t R, int64_t N, int64_t K) {
     if (M < 0 || R < 0 || N < 0 || K < 0 || M > kMaxRows || R > kMaxRows || N > kMaxRows || K > kMaxK) return 0;
-    if (mx_linear_grouped_casts(R, N, up(K, 128))) return 0;
+    // the groups' number, which may make it needless, is not known here
+    if (mx_linear_grouped_casts(R, 0, N, up(K, 128))) return 0;
     return M * (up(K, 128) / 2) + up(M, 128) * (up(K, 128) / 32);
 }
 
@@ -252,7 +253,7 @@ nvfp4_status nvfp4_mx_linear_grouped(const void* x, nvfp4_dtype x_type, int64_t 
     uint8_t* q = (uint8_t*)workspace;
     uint8_t* sf = q + M * (up(K, 128) / 2);
     const MxCast c{x, x_type, M, K, ldx, nullptr, M, nullptr, 0, q, sf, nullptr, nullptr};
-    const bool casts = mx_linear_grouped_casts(R, N, up(K, 128));
+    const bool casts = mx_linear_grouped_casts(R, num_groups, N, up(K, 128));
     if (K > 0 && !casts && (s = check_hip(launch_mx_cast(c, as_stream(stream)), "mx cast")) != NVFP4_OK) return s;
     const MxGemm g{q, sf, M, w_q, w_sf, R, N, up(K, 128), out_type, out, offsets, num_groups, rows, row_scale};
     return (s = check_hip(casts ? launch_mx_linear(g, c, as_stream(stream)) : launch_mx_gemm(g, as_stream(stream)),

@@ -831,10 +831,14 @@ constexpr int64_t kFewOutputs = int64_t(1) << 19;
 
 // Whether the product casts x itself instead of in a launch before it.  Each
 // workgroup casts its own rows, so that costs time with rows x workgroups x K;
-// the launch it saves costs the GPU 4 us and the host 3.5.  A call, with and
-// without: 16 x 4096 -> 4096 (2^24 elements cast) 8.5 us and 10.5, 8 x 8192 ->
-// 8192 (2^25) 13.5 and 10.7; 256 rows of 1024 over 16 experts of 2048 (2^24)
-// 12.5 and 13.0, 903 rows of 1000 over 33 of 777 (23 million) 19.9 and 12.2.
+// the launch it saves costs the GPU 3 us and the host 3.5.  A call, with and
+// without: 16 x 4096 -> 4096 (2^24 elements cast) 7.1 us and 11.1, 8 x 8192 ->
+// 8192 (2^24) 10.9 and 11.3, 8 x 8192 -> 28672 (2^26) 33.6 and 28.0; 256 rows of
+// 1024 over 16 experts of 2048 (2^24) 12.3 and 13.0, 903 rows of 1000 over 33 of
+// 777 (23 million) 19.9 and 13.1.  Groups of up to two rows on average take it
+// in any case: the weights bound them, and tiles would be nearly empty (64 and
+// 128 rows of 4096 over 64 experts of 4096 57.9 and 76.9 us, in tiles 64.5 and
+// 80.2; at four rows 101 and 92).
 constexpr int64_t kCastWork = int64_t(1) << 24;
 constexpr int kCastRows = 16;             // rows to a workgroup at most
 constexpr int64_t kCastGroupedRows = 1024;
@@ -849,8 +853,9 @@ bool mx_linear_casts(int64_t M, int64_t N, int64_t Kp) {
     return M <= (most < kCastRows ? most : kCastRows) && M * ((N + cols - 1) / cols) <= kCastWork / (Kp > 0 ? Kp : 1);
 }
 
-bool mx_linear_grouped_casts(int64_t R, int64_t N, int64_t Kp) {
-    return R <= kCastGroupedRows && cast_rows(Kp / kMxStep) >= 8 && R * ((N + 31) / 32) <= kCastWork / (Kp > 0 ? Kp : 1);
+bool mx_linear_grouped_casts(int64_t R, int64_t E, int64_t N, int64_t Kp) {
+    return R <= kCastGroupedRows && cast_rows(Kp / kMxStep) >= 8 &&
+           (R <= 2 * E || R * ((N + 31) / 32) <= kCastWork / (Kp > 0 ? Kp : 1));
 }
 
 hipError_t launch_mx_gemm(const MxGemm& g, hipStream_t st) {

@@ -165,6 +165,20 @@ def test_grouped_rows_and_factors(E, R, N, K):
         mx_ref.check_product(lin[s:e], av, bv, f[s:e].astype(np.float64))
 
 
+def test_few_rows_to_many_large_experts():
+    # up to two rows a group on average, whatever the work of casting them
+    rng = np.random.default_rng(12)
+    E, R, N, K = 64, 100, 1400, 4000
+    off, x = groups(rng, E, R), data(rng, R, K, torch.bfloat16, wild=False)
+    (q0, s0, b0), (q1, s1, b1) = vectors(rng, N, K), vectors(rng, N, K)
+    bq, bsf = torch.stack([q0, q1] * (E // 2)), torch.stack([s0, s1] * (E // 2))
+    a = np.pad(mx_ref.fake(mx_ref.host64(x)), ((0, 0), (0, b0.shape[1] - K)))
+    got = nv.mx_linear_grouped(x, bq, bsf, torch.from_numpy(off).cuda(), out_dtype=torch.float32)
+    for e in range(E):
+        if off[e + 1] > off[e]:
+            mx_ref.check_product(got[off[e]:off[e + 1]], a[off[e]:off[e + 1]], (b0, b1)[e % 2])
+
+
 def test_an_outside_row_is_zero_beside_a_nan():
     # the row that stands in for an index outside must not leak its NaN
     rng = np.random.default_rng(8)
